@@ -6,4 +6,4 @@ C-ABI library ``libgemv_fused.so`` (hand-written HIP for gfx950); the
 ``binding`` module marshals torch tensors into it.  ``synth`` holds the
 seeded synthetic inputs and the weight packers.
 """
-__all__ = ["binding", "synth"]
+__all__ = ["binding", "paged", "synth"]
