@@ -21,9 +21,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = [os.path.join(CSRC, "gemv_kernels.hip"), os.path.join(CSRC, "gemv_cols.hip"),
            os.path.join(CSRC, "gemv_validate.cpp"), os.path.join(CSRC, "gemv_fwht.hip"),
-           os.path.join(CSRC, "gemv_mfma.hip"), os.path.join(CSRC, "paged_validate.cpp"),
-           os.path.join(CSRC, "paged_slots.hip"), os.path.join(CSRC, "paged_append.hip"),
-           os.path.join(CSRC, "paged_attn.hip")]
+           os.path.join(CSRC, "gemv_mfma.hip"), *(os.path.join(CSRC, "paged", f) for f in (
+               "paged_validate.cpp", "paged_slots.hip", "paged_append.hip", "paged_attn.hip"))]
 PROBE_SOURCES = [os.path.join(CSRC, "hbm_probe.hip")]
 CPU_SOURCE = os.path.join(HERE, "cpu", "cpu_fused.c")
 CPU_LIB = os.path.join(HERE, "libcpu_fused.so")

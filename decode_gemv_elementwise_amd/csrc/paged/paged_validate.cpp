@@ -216,9 +216,9 @@ int validate_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, 
         return GEMV_E_FMT;
     if (cache->dim != 64 && cache->dim != 128 && cache->dim != 256)
         return GEMV_E_DIM;
-    if (requests < 1 || requests > kPagedMaxRequests || tokens < 0 || table_width < 1 || table_width > kInt ||
-        q_heads < 1 || q_heads > GEMV_PAGED_MAX_HEADS || q_heads % cache->heads != 0 || tokens * q_heads > kInt ||
-        tokens > kInt || window < 0 || window > kInt || sinks < 0 || sinks > kInt || workspace_bytes < 0 ||
+    if (requests < 1 || requests > kPagedMaxRequests || tokens < 0 || tokens > kInt || table_width < 1 ||
+        table_width > kInt || q_heads < 1 || q_heads > GEMV_PAGED_MAX_HEADS || q_heads % cache->heads != 0 ||
+        tokens * q_heads > kInt || window < 0 || window > kInt || sinks < 0 || sinks > kInt || workspace_bytes < 0 ||
         !std::isfinite(scale))
         return GEMV_E_DIM;
     if (table_stride < (requests > 1 ? table_width : 1) || table_stride > kInt)
