@@ -32,21 +32,21 @@ __device__ __forceinline__ uint32_t add_cut(uint32_t a, uint32_t b, uint32_t cap
 // Exclusive prefix of v over a workgroup of WAVES waves; *total gets the whole
 // sum.  `scratch` holds WAVES words and is free again after the caller's next
 // barrier.
-template <int WAVES, class Add>
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *scratch, uint32_t *total, Add add)
+template <int WAVES, class T, class Add>
+__device__ __forceinline__ T block_prefix(T v, T *scratch, T *total, Add add)
 {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    uint32_t s = v;
+    T s = v;
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t o = __shfl_up(s, d);
+        const T o = __shfl_up(s, d);
         if (lane >= d)
             s = add(o, s);
     }
     if (lane == kWave - 1)
         scratch[wave] = s;
     __syncthreads();
-    uint32_t base = 0, all = 0;
+    T base = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
         if (w == wave)
@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *scratch, 
         all = add(all, scratch[w]);
     }
     *total = all;
-    const uint32_t before = __shfl_up(s, 1);
+    const T before = __shfl_up(s, 1);
     return lane == 0 ? base : add(base, before);
 }
 

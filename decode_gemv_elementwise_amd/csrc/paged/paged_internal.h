@@ -27,13 +27,15 @@ inline FastDiv fast_div(int64_t d)
 
 constexpr int64_t kPagedMaxRequests = 1 << 20;
 
-// The attention's workspace: a counter per split group, then the parts.  A part
-// holds one workgroup's share of the keys of one row tile: the rows' sums over
-// v (dim floats a row), then their maxima, then their weight sums.
-constexpr int kAttnRows = 16;         // rows of a tile of few rows
-constexpr int kAttnParts = 2048;      // parts that a launch can fill
-constexpr int kAttnCounters = kAttnParts;
-constexpr int64_t attn_part_floats(int dim) { return (int64_t)kAttnRows * (dim + 2); }
+// The attention's workspace: a counter for every workgroup, then the parts, two
+// places for every workgroup.  A part holds one workgroup's share of the keys of
+// one row tile: the rows' sums over v, their maxima and their weight sums.
+constexpr int kAttnRows = 16; // rows of a tile of few rows
+constexpr int kAttnCounters = 2048;
+constexpr int64_t kAttnGroups = 512; // workgroups of a launch: as many as the 256 compute units hold at once
+// Floats of the largest part: 128 rows of up to 128 values (half as many of 256),
+// and a maximum and a sum of each lane.
+constexpr int64_t attn_part_floats(int64_t dim) { return 128 * (dim < 128 ? dim : 128) + 512; }
 
 int validate_slots(const int32_t *cached, const int32_t *fresh, int64_t requests, const int32_t *free_pages,
                    int64_t num_free, int64_t page_size, int32_t *block_table, int64_t table_width,

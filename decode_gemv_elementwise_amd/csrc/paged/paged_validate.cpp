@@ -251,7 +251,7 @@ int64_t attn_workspace(int64_t dim)
 {
     if (dim != 64 && dim != 128 && dim != 256)
         return GEMV_E_DIM;
-    return kAttnCounters * 4 + (int64_t)kAttnParts * attn_part_floats((int)dim) * 4;
+    return kAttnCounters * 4 + 2 * kAttnGroups * attn_part_floats(dim) * 4;
 }
 
 } // namespace gemv
