@@ -15,7 +15,7 @@
 // The host does not know the lengths, so every workgroup works the plan out from
 // them: the blocks of keys of all tiles form one line (request, head, tile,
 // block), from a prefix sum over the requests, and workgroup w takes the w-th
-// equal share of it, whatever tiles that cuts.  A tile whose keys are cut leaves
+// equal share of it, whatever tiles that cuts (but for slivers).  A tile whose keys are cut leaves
 // its parts in the workspace; the workgroup that counts the last of them joins
 // them in order, so the result does not depend on which came last.
 #include <cfloat>
@@ -28,7 +28,10 @@ namespace gemv {
 namespace {
 
 constexpr int kFewShare = 8;   // blocks of 32 keys that a workgroup takes at least
-constexpr int kManyShare = 16; // the same where any tile has many rows
+constexpr int kManyShare = 8;  // the same where any tile has many rows
+// A share's end this near a tile's edge moves to it: starting on a tile, and
+// joining its parts, cost about as much as so many blocks.
+constexpr uint32_t kFewEdge = 8, kManyEdge = 12;
 constexpr uint32_t kMostCost = INT_MAX;
 
 __device__ __forceinline__ bool is_few(const AttnArgs &a, const Request &q) { return (int64_t)q.n * a.group <= kFewRows; }
@@ -74,7 +77,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(AttnArgs)
     __shared__ __align__(16) char va[kBuffer];
     __shared__ __align__(16) char kb[kBuffer];
     __shared__ __align__(16) char vb[kBuffer];
-    __shared__ uint32_t before[kThreads], scratch[kWaves];
+    __shared__ uint32_t before[kThreads], scratch[kWaves], flags[kWaves];
     __shared__ Request requests[kThreads];
 
     // The line's length: requests that do not share rows stay below kMostCost (the
@@ -90,41 +93,52 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(AttnArgs)
             cost = sum(cost, min((uint64_t)tiles_of<D>(a, q) * a.heads * cost_of<D>(a, q), (uint64_t)kMostCost));
             many = many || !is_few(a, q);
         }
-        block_prefix<kWaves>(cost, scratch, &total, sum);
-        many = __syncthreads_or(many);
+        block_prefix<kWaves>(threadIdx.x, cost, scratch, &total, sum);
+        total = uniform(total);
+        many = any_thread(threadIdx.x, many, flags);
     }
 
     // this workgroup's share [x, x1): every group has `each` places, the first `more` one in addition
     uint32_t base = 0, x = 0, x1 = 0, each = 0, more = 0;
     int stride = 0;
-    bool split = false;
-    const uint32_t w = blockIdx.x;
+    uint32_t edge = 0;
+    // Neighbouring shares go to one of the 8 dies, which share an L2 cache; and where
+    // a compute unit holds two workgroups, w and w + 256 in order of launch, the
+    // second half of a die's shares goes backwards: later tiles of a chunk see more
+    // keys, so a unit gets a long and a short one.
+    uint32_t w = blockIdx.x;
+    if (gridDim.x == kAttnGroups) {
+        constexpr uint32_t per = kAttnGroups / 8;
+        const uint32_t i = w / 8;
+        w = w % 8 * per + (i < per / 2 ? i : per + per / 2 - 1 - i);
+    }
     for (int r0 = 0; r0 < a.requests; r0 += kThreads) {
-        const int r = r0 + threadIdx.x;
+        const int thread = thread_here(), r = r0 + thread;
         Request q{0, 0, 0};
         if (r < a.requests)
             q = request_of(a, r);
         uint32_t here;
-        before[threadIdx.x] = block_prefix<kWaves>(
-            (uint32_t)min((uint64_t)tiles_of<D>(a, q) * a.heads * cost_of<D>(a, q), (uint64_t)kMostCost), scratch, &here, sum);
-        requests[threadIdx.x] = q;
-        const bool any = __syncthreads_or(!is_few(a, q));
+        before[thread] = block_prefix<kWaves>(
+            thread, (uint32_t)min((uint64_t)tiles_of<D>(a, q) * a.heads * cost_of<D>(a, q), (uint64_t)kMostCost), scratch, &here, sum);
+        requests[thread] = q;
+        here = uniform(here);
+        const bool any = any_thread(thread, !is_few(a, q), flags);
         if (r0 == 0) {
             if (once) {
                 total = here;
                 many = any;
             }
             const uint32_t share = many ? kManyShare : kFewShare;
-            const uint32_t groups = min(gridDim.x, (total + share - 1) / share);
+            const uint32_t groups = uniform(min(gridDim.x, (total + share - 1) / share));
             if (w >= groups || total == kMostCost)
                 return;
-            each = total / groups;
+            each = uniform(total / groups);
             more = total - each * groups;
             x = w * each + min(w, more);
             x1 = x + each + (w < more);
-            // cut anywhere if the parts have room: two for each workgroup, below 2^28 floats in all
+            // a tile is cut only if the parts have room: two for each workgroup, below 2^28 floats in all
             stride = many ? many_part(D) : few_part(D);
-            split = a.part_room >= 2 * (int64_t)groups * stride;
+            edge = a.part_room < 2 * (int64_t)groups * stride ? kMostCost / 2 : many ? kManyEdge : kFewEdge;
         }
         while (x < x1 && x < base + here) {
             int lo = 0, hi = min(kThreads, a.requests - r0);
@@ -137,26 +151,25 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(AttnArgs)
             }
             lo = uniform(lo);
             const Request q = {(int)uniform(requests[lo].q0), (int)uniform(requests[lo].n), (int)uniform(requests[lo].kv)};
-            const uint32_t y = x - base - uniform(before[lo]), nb = cost_of<D>(a, q), tiles = tiles_of<D>(a, q);
+            const uint32_t y = x - base - uniform(before[lo]), nb = uniform(cost_of<D>(a, q)), tiles = uniform(tiles_of<D>(a, q));
             const uint32_t unit = uniform(y / nb), start = x - (y - unit * nb); // of the tile
-            Share sh{(int)(x - start), 0, (int)nb, 1, 0, 0, stride};
-            if (!split) { // a tile goes whole to the workgroup whose share it begins in
-                x = start + nb;
-                if (sh.b > 0)
-                    continue;
-                sh.len = nb;
-            } else {
-                sh.len = min(x1 - start, nb) - sh.b;
-                x += sh.len;
-                if (sh.len < (int)nb) {
-                    const auto group_of = [&](uint32_t place) {
-                        const uint32_t longer = more * (each + 1);
-                        return uniform(place < longer ? place / (each + 1) : more + (place - longer) / each);
-                    };
-                    sh.first = group_of(start);
-                    sh.np = group_of(start + nb - 1) - sh.first + 1;
-                    sh.me = w - sh.first;
-                }
+            // both ends of the share, as places of this tile; one near an edge of it moves there
+            const auto moved = [&](uint32_t b) {
+                return b >= nb ? nb : b < edge && b <= nb - b ? 0 : nb - b < edge && nb - b < b ? nb : b;
+            };
+            const uint32_t b0 = moved(x - start), b1 = moved(x1 - start);
+            x = start + nb;
+            if (b0 >= b1)
+                continue;
+            Share sh{(int)b0, (int)(b1 - b0), (int)nb, 1, 0, 0, stride};
+            if (sh.len < (int)nb) {
+                const auto group_of = [&](uint32_t place) {
+                    const uint32_t longer = more * (each + 1);
+                    return uniform(place < longer ? place / (each + 1) : more + (place - longer) / each);
+                };
+                sh.first = group_of(start + edge - 1);
+                sh.np = group_of(start + nb - edge) - sh.first + 1;
+                sh.me = w - sh.first;
             }
             const int head = uniform(unit / tiles), tile = unit - head * tiles;
             if (is_few(a, q))

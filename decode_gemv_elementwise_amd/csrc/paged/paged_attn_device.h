@@ -48,6 +48,21 @@ __device__ __forceinline__ int thread_here()
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// True for every thread if it is for one.  flags: a word a wave, free again after
+// the caller's next barrier.
+__device__ __forceinline__ bool any_thread(int thread, bool x, uint32_t *flags)
+{
+    const uint32_t mine = __any(x);
+    if ((thread & (kWave - 1)) == 0)
+        flags[thread / kWave] = mine;
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+        all |= flags[w];
+    return uniform(all);
+}
+
 template <bool BF> __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
 {
     if constexpr (BF)
@@ -156,12 +171,19 @@ __device__ __forceinline__ bool sees_all(const AttnArgs &a, int p_lo, int p_hi, 
     return j0 + n - 1 <= p_lo && (a.window == 0 || j0 > p_hi - a.window || j0 + n <= a.sinks);
 }
 
-// The page id of key j, -1 where there is none.
-__device__ __forceinline__ int id_of(const AttnArgs &a, const int32_t *table, int j)
+// The page id of key j as the table has it, -1 past the table's end; and -1 for
+// one that is no page.
+__device__ __forceinline__ int raw_id(const AttnArgs &a, const int32_t *table, int j)
 {
     const uint32_t at = div_by(a.page, j);
-    const int id = at < (uint32_t)a.width ? table[at] : -1;
-    return (unsigned)id < (unsigned)a.num_pages ? id : -1;
+    return at < (uint32_t)a.width ? table[at] : -1;
+}
+
+__device__ __forceinline__ int checked_id(const AttnArgs &a, int id) { return (unsigned)id < (unsigned)a.num_pages ? id : -1; }
+
+__device__ __forceinline__ int id_of(const AttnArgs &a, const int32_t *table, int j)
+{
+    return checked_id(a, raw_id(a, table, j));
 }
 
 // Element offset of key j in page id (a key without a page reads page 0, and
@@ -218,11 +240,11 @@ struct Parts {
 // Counts this workgroup's part as written; true for the one that came last.
 // Every wave waits until its stores are where all units see them, then the
 // barrier, then thread 0 counts.
-__device__ __forceinline__ bool last_part(const AttnArgs &a, const Share &sh, int *lds)
+__device__ __forceinline__ bool last_part(const AttnArgs &a, const Share &sh, int thread, int *lds)
 {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (thread == 0) {
         const int before = __hip_atomic_fetch_add(a.counters + sh.first, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         *lds = before == sh.np - 1;
         if (before == sh.np - 1) // ready for the next call

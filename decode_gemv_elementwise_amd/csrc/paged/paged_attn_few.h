@@ -83,60 +83,82 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
             o[i] = f32x4{0, 0, 0, 0};
     }
 
-    // Page ids of a block's keys that this lane reads: of k the keys krun and
-    // krun + 4, of v the eight from vrun on.
-    __device__ __forceinline__ void ids_of(int j0, int *kid, int *vid) const
+    // Page ids of a block's keys that this lane reads, as the table has them (they
+    // are checked where they are used, so that their load is waited for there): of
+    // k the keys krun and krun + 4, of v the eight from vrun on.
+    struct Ids {
+        int k[NK], v[NV];
+    };
+    // A block's k and v as this lane needs them; bit i of has: v's key vrun + i has a page.
+    struct Data {
+        u32x4 k[2][KS];
+        uint32_t v[8][VW];
+        uint32_t has;
+    };
+
+    __device__ __forceinline__ int krun(int j0) const { return j0 + 8 * (col >> 2) + (col & 3); }
+    __device__ __forceinline__ int vrun(int j0) const { return j0 + 8 * grp; }
+
+    __device__ __forceinline__ void load_ids(int j0, Ids &ids) const
     {
-        const int krun = j0 + 8 * (col >> 2) + (col & 3), vrun = j0 + 8 * grp;
 #pragma unroll
         for (int i = 0; i < NK; ++i)
-            kid[i] = id_of(a, table, krun + 4 * i);
+            ids.k[i] = raw_id(a, table, krun(j0) + 4 * i);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            vid[i] = id_of(a, table, vrun + i);
+            ids.v[i] = raw_id(a, table, vrun(j0) + i);
     }
 
-    __device__ __forceinline__ void block(int j0, const int *kid, const int *vid)
+    // Asks for a block's k and v.
+    __device__ __forceinline__ void load(int j0, const Ids &ids, Data &x) const
     {
-        const int krun = j0 + 8 * (col >> 2) + (col & 3), vrun = j0 + 8 * grp;
-        u32x4 kf[2][KS];
+        const uint16_t *kp = kbase + 8 * grp, *vp = vbase + VPL * col;
+        if constexpr (PAGE8) { // a run of eight lies in one page
+            kp += key_offset(a, a.k_stride, checked_id(a, ids.k[0]), krun(j0));
+            vp += key_offset(a, a.v_stride, checked_id(a, ids.v[0]), vrun(j0));
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint16_t *src = kbase + key_offset(a, a.k_stride, kid[PAGE8 ? 0 : i], krun + 4 * i) + 8 * grp;
+            const uint16_t *src = PAGE8 ? kp + 4 * i * a.k_stride[1]
+                                        : kp + key_offset(a, a.k_stride, checked_id(a, ids.k[PAGE8 ? 0 : i]), krun(j0) + 4 * i);
 #pragma unroll
             for (int s = 0; s < KS; ++s)
-                kf[i][s] = *reinterpret_cast<const u32x4 *>(src + 32 * s);
+                x.k[i][s] = *reinterpret_cast<const u32x4 *>(src + 32 * s);
         }
-        uint32_t vw[8][VW];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint16_t *src = vbase + key_offset(a, a.v_stride, vid[PAGE8 ? 0 : i], vrun + i) + VPL * col;
+            const uint16_t *src = PAGE8 ? vp + i * a.v_stride[1]
+                                        : vp + key_offset(a, a.v_stride, checked_id(a, ids.v[PAGE8 ? 0 : i]), vrun(j0) + i);
             if constexpr (VW == 2) {
-                const u32x2 x = *reinterpret_cast<const u32x2 *>(src);
-                vw[i][0] = x[0];
-                vw[i][1] = x[1];
+                const u32x2 y = *reinterpret_cast<const u32x2 *>(src);
+                x.v[i][0] = y[0];
+                x.v[i][1] = y[1];
             } else {
 #pragma unroll
                 for (int w = 0; w < VW; w += 4) {
-                    const u32x4 x = *reinterpret_cast<const u32x4 *>(src + 2 * w);
+                    const u32x4 y = *reinterpret_cast<const u32x4 *>(src + 2 * w);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        vw[i][w + e] = x[e];
+                        x.v[i][w + e] = y[e];
                 }
             }
         }
-        uint32_t has = 0; // bit i: v's key vrun + i has a page
+        x.has = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            has |= (uint32_t)(vid[PAGE8 ? 0 : i] >= 0) << i;
+            x.has |= (uint32_t)(checked_id(a, ids.v[PAGE8 ? 0 : i]) >= 0) << i;
+        __builtin_amdgcn_sched_barrier(0); // all are asked for before anything waits for one
+    }
 
+    __device__ __forceinline__ void block(int j0, Data &x)
+    {
         float p[8];
         {
             f32x4 s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                s0 = mfma16<BF>(kf[0][s], qf[s], s0);
-                s1 = mfma16<BF>(kf[1][s], qf[s], s1);
+                s0 = mfma16<BF>(x.k[0][s], qf[s], s0);
+                s1 = mfma16<BF>(x.k[1][s], qf[s], s1);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -145,11 +167,11 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
             }
         }
         // every row of the tile sees every key of the block
-        const bool whole = sees_all(a, p_lo, p_hi, j0, kFewBlock) && !__any(has != 0xff);
+        const bool whole = sees_all(a, p_lo, p_hi, j0, kFewBlock) && !__any(x.has != 0xff);
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                p[i] = (has >> i & 1) && sees(a, p_row, vrun + i) ? p[i] : kNegInf;
+                p[i] = (x.has >> i & 1) && sees(a, p_row, vrun(j0) + i) ? p[i] : kNegInf;
         }
         float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
         top = fmaxf(m, row_max(top));
@@ -176,11 +198,11 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
             uint32_t bad = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool keep = (has >> i & 1) && vrun + i <= p_hi;
+                const bool keep = (x.has >> i & 1) && vrun(j0) + i <= p_hi;
 #pragma unroll
                 for (int w = 0; w < VW; ++w) {
-                    vw[i][w] = keep ? vw[i][w] : 0;
-                    bad |= not_finite<BF>(vw[i][w]);
+                    x.v[i][w] = keep ? x.v[i][w] : 0;
+                    bad |= not_finite<BF>(x.v[i][w]);
                 }
             }
             special = __any(bad != 0);
@@ -189,8 +211,8 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int w = 0; w < VW; ++w) {
-                        const uint32_t n = not_finite<BF>(vw[i][w]);
-                        vw[i][w] &= ~((n >> 15) * 0xffffu);
+                        const uint32_t n = not_finite<BF>(x.v[i][w]);
+                        x.v[i][w] &= ~((n >> 15) * 0xffffu);
                     }
             }
         }
@@ -206,7 +228,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
             u32x4 vf;
 #pragma unroll
             for (int w = 0; w < 4; ++w)
-                vf[w] = __builtin_amdgcn_perm(vw[2 * w + 1][i / 2], vw[2 * w][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+                vf[w] = __builtin_amdgcn_perm(x.v[2 * w + 1][i / 2], x.v[2 * w][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
             o[i] = mfma16<BF>(vf, pf, o[i]);
             if constexpr (F32OUT)
                 o[i] = mfma16<BF>(vf, pl, o[i]);
@@ -257,20 +279,45 @@ __device__ __forceinline__ void run_few(const AttnArgs &a, const Request &rq, in
     // shares begin at whole rounds of the waves
     const int b0 = sh.from(walk.count) & -kWaves;
     const int b1 = sh.b + sh.len == sh.nb ? walk.count : sh.to(walk.count) & -kWaves;
-    int kid[t.NK], vid[t.NV];
-    if (b0 + wave < b1)
-        t.ids_of(walk.block(b0 + wave) * kFewBlock, kid, vid);
-    for (int b = b0 + wave; b < b1; b += kWaves) {
-        int nkid[t.NK], nvid[t.NV];
-        if (b + kWaves < b1)
-            t.ids_of(walk.block(b + kWaves) * kFewBlock, nkid, nvid);
-        t.block(walk.block(b) * kFewBlock, kid, vid);
-#pragma unroll
-        for (int i = 0; i < t.NK; ++i)
-            kid[i] = nkid[i];
-#pragma unroll
-        for (int i = 0; i < t.NV; ++i)
-            vid[i] = nvid[i];
+    const auto key = [&](int b) { return walk.block(b) * kFewBlock; };
+    // A block's page ids are asked for two rounds ahead and its k and v one round
+    // ahead (the widest heads have no registers for that).
+    int b = b0 + wave;
+    typename decltype(t)::Ids ids;
+    if (b < b1)
+        t.load_ids(key(b), ids);
+    if constexpr (D == 256) {
+        for (; b < b1; b += kWaves) {
+            typename decltype(t)::Ids next;
+            if (b + kWaves < b1)
+                t.load_ids(key(b + kWaves), next);
+            typename decltype(t)::Data x;
+            t.load(key(b), ids, x);
+            t.block(key(b), x);
+            ids = next;
+        }
+    } else {
+        typename decltype(t)::Data x, y;
+        // asks for block b's k and v and the ids of the one after
+        const auto ahead = [&](int b, auto &x) {
+            if (b < b1) {
+                const auto now = ids;
+                if (b + kWaves < b1)
+                    t.load_ids(key(b + kWaves), ids);
+                t.load(key(b), now, x);
+            }
+        };
+        ahead(b, x);
+        while (b < b1) {
+            ahead(b + kWaves, y);
+            t.block(key(b), x);
+            b += kWaves;
+            if (b >= b1)
+                break;
+            ahead(b + kWaves, x);
+            t.block(key(b), y);
+            b += kWaves;
+        }
     }
 
     // join the waves
@@ -327,7 +374,7 @@ __device__ __forceinline__ void run_few(const AttnArgs &a, const Request &rq, in
                 parts.put(mine + kFewRows * D + kFewRows + row, sum);
             }
         }
-        if (!last_part(a, sh, &lds_last))
+        if (!last_part(a, sh, thread, &lds_last))
             return;
         // 16 threads to a row again; what rows the tile lacks gives the others
         // more threads, each set of them taking every sets-th part

@@ -63,6 +63,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
     static constexpr int kFetch = kBlock / (kRun * kWaves);   // such instructions of a wave per block
     static constexpr int KS = D / 16;                             // k steps of the first product
     static constexpr int kHalves = many_halves(D), DW = D / kHalves, DT = DW / 32; // values of a wave, tiles of them
+    static constexpr int kAhead = 2; // products between a read of LDS and its use
     // binary16's weights are lifted, which leaves one power of two to its largest
     static constexpr float kSlack = BF ? 8.0f : 1.0f;
 
@@ -95,8 +96,8 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
     __device__ __forceinline__ void begin(const Request &rq, int r, int tile, int head)
     {
         thread = thread_here();
-        lane = thread & (kWave - 1);
         wave = uniform(thread / kWave);
+        lane = thread & (kWave - 1);
         col = lane & 31;
         half = lane >> 5;
         values = wave % kHalves * DW;
@@ -157,7 +158,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
     // last row and keys without a page hold anything and are taken as 0, and an
     // infinity or NaN of a key that only some rows see is taken out (true if there
     // was one: add_special adds it for the rows that see it).
-    __device__ __forceinline__ bool clean(int j0, uint64_t has, char *v) const
+    __device__ __forceinline__ bool clean(int j0, uint64_t has, char *v, uint32_t *flags) const
     {
         uint32_t bad = 0;
         for (int at = thread; at < kBlock * kChunks; at += kThreads) {
@@ -176,7 +177,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
             if (drop)
                 *reinterpret_cast<u32x4 *>(v + at * 16) = x;
         }
-        return __syncthreads_or(bad != 0);
+        return any_thread(thread, bad != 0, flags);
     }
 
     // Bit i: this lane's row sees key j0 + i.
@@ -199,17 +200,28 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
         asm volatile("" : "+v"(ln));
         f32x16 s[KT];
         {
-            const char *row = k + (ln & 31) * kRowBytes;
+            const int row = (ln & 31) * kRowBytes;
             const int turn = 16 * ((ln >> 5) ^ k_turn(ln & 31));
 #pragma unroll
             for (int t = 0; t < KT; ++t)
                 s[t] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+            // rows 32 apart have the same turn
+            const auto read = [&](int n) {
+                return *reinterpret_cast<const u32x4 *>(k + (row + n % KT * 32 * kRowBytes + (turn ^ (32 * (n / KT)))));
+            };
+            u32x4 f[kAhead];
 #pragma unroll
-            for (int i = 0; i < KS; ++i)
+            for (int n = 0; n < kAhead; ++n)
+                f[n] = read(n);
+            // the order is kept: left alone, the compiler waits for each read in turn
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = 0; t < KT; ++t) // rows 32 apart have the same turn
-                    s[t] = mfma32<BF>(*reinterpret_cast<const u32x4 *>(row + t * 32 * kRowBytes + (turn ^ (32 * i))), qf[i],
-                                      s[t]);
+            for (int n = 0; n < KS * KT; ++n) {
+                s[n % KT] = mfma32<BF>(f[n % kAhead], qf[n / KT], s[n % KT]);
+                if (n + kAhead < KS * KT)
+                    f[n % kAhead] = read(n + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         if constexpr (PART) {
             // by masks of all bits, not by comparisons: 32 of those would take 64 scalar registers
@@ -260,21 +272,29 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
         {
             // 16 lanes bring 4 keys by 16 values
             const int key = 4 * (ln >> 5) + ((ln & 15) >> 2), chunk = 2 * ((ln >> 4) & 1) + ((ln & 3) >> 1);
-            const char *row = v + key * kRowBytes + 2 * values + 8 * (ln & 1);
+            const int row = key * kRowBytes + 2 * values + 8 * (ln & 1);
             const int turn = 16 * (chunk ^ v_turn(key));
+            const auto read = [&](int n) { // rows 8 apart have the same turn
+                const int at = row + 16 * (n / DT) * kRowBytes + (turn ^ (64 * (n % DT)));
+                const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(v + at));
+                const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(v + (at + 8 * kRowBytes)));
+                const u32x2 lo = __builtin_bit_cast(u32x2, x), hi = __builtin_bit_cast(u32x2, y);
+                return u32x4{lo[0], lo[1], hi[0], hi[1]};
+            };
+            u32x4 f[kAhead];
 #pragma unroll
-            for (int t = 0; t < 2 * KT; ++t)
+            for (int n = 0; n < kAhead; ++n)
+                f[n] = read(n);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const char *at = row + 16 * t * kRowBytes + (turn ^ (64 * d)); // rows 8 apart have the same turn
-                    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at);
-                    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 8 * kRowBytes));
-                    const u32x2 lo = __builtin_bit_cast(u32x2, x), hi = __builtin_bit_cast(u32x2, y);
-                    const u32x4 vf = {lo[0], lo[1], hi[0], hi[1]};
-                    o[d] = mfma32<BF>(vf, pf[t], o[d]);
-                    if constexpr (F32OUT)
-                        o[d] = mfma32<BF>(vf, pl[t], o[d]);
-                }
+            for (int n = 0; n < 2 * KT * DT; ++n) {
+                o[n % DT] = mfma32<BF>(f[n % kAhead], pf[n / DT], o[n % DT]);
+                if constexpr (F32OUT)
+                    o[n % DT] = mfma32<BF>(f[n % kAhead], pl[n / DT], o[n % DT]);
+                if (n + kAhead < 2 * KT * DT)
+                    f[n % kAhead] = read(n + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         if constexpr (PART)
             if (special)
@@ -326,6 +346,7 @@ __device__ __forceinline__ void run_many(const AttnArgs &a, const Request &rq, i
     constexpr int DT = D / many_halves(D) / 32, kBlock = many_block(D);
     constexpr uint64_t kAll = kBlock == 64 ? ~0ull : (1ull << kBlock % 64) - 1; // every key of a block has a page
     __shared__ int lds_last;
+    __shared__ uint32_t flags[kWaves];
     ManyRows<BF, D, F32OUT, PAGE8> t(a);
     t.begin(rq, r, tile, head);
     const Walk walk = walk_of<kBlock>(a, t.p_lo, t.p_hi);
@@ -334,43 +355,39 @@ __device__ __forceinline__ void run_many(const AttnArgs &a, const Request &rq, i
     auto key = [&](int b) { return walk.block(b) * kBlock; };
     // ids of the block after next, and which keys of this and the next have a page
     // (an id is checked where it is used, so that its load is waited for there)
-    auto id_at = [&](int b) {
-        const uint32_t at = div_by(a.page, key(b) + t.lane);
-        return at < (uint32_t)a.width ? t.table[at] : -1;
-    };
-    auto checked = [&](int id) { return (unsigned)id < (unsigned)a.num_pages ? id : -1; };
-    int ids = b0 < b1 ? checked(id_at(b0)) : -1;
+    const auto id_at = [&](int b) { return raw_id(a, t.table, key(b) + t.lane); };
+    int ids = b0 < b1 ? checked_id(a, id_at(b0)) : -1;
     uint64_t has = 0, has_next = __ballot(ids >= 0);
     if (b0 < b1)
         t.fetch(key(b0), ids, ka, va);
     if (b0 + 1 < b1)
         ids = id_at(b0 + 1);
-    for (int b = b0; b < b1; ++b) {
-        const bool odd = (b - b0) & 1;
+    // The buffers by name in two copies of the step: the compiler then knows that
+    // reads of one need not wait for the copy into the other.
+    const auto step = [&](int b, char *k, char *v, char *knext, char *vnext) {
         const int j0 = key(b);
         has = has_next;
         __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt(0): this wave's rows of the block are in LDS
         __syncthreads();                    // everyone's are, and everyone is done with the other buffers
         if (b + 1 < b1) {
-            ids = checked(ids);
+            ids = checked_id(a, ids);
             has_next = __ballot(ids >= 0);
-            if (odd)
-                t.fetch(key(b + 1), ids, ka, va);
-            else
-                t.fetch(key(b + 1), ids, kb, vb);
+            t.fetch(key(b + 1), ids, knext, vnext);
             if (b + 2 < b1)
                 ids = id_at(b + 2);
         }
         if (!sees_all(a, t.p_lo, t.p_hi, j0, kBlock) || (has & kAll) != kAll) {
-            const bool special = t.clean(j0, has, odd ? vb : va);
+            const bool special = t.clean(j0, has, v, flags);
             if (t.live && j0 <= t.w_hi)
-                t.template block<true>(j0, has, odd ? kb : ka, odd ? vb : va, special);
-        } else if (t.live) { // the buffers by name: reads of one need not wait for copies into the other
-            if (odd)
-                t.template block<false>(j0, has, kb, vb, false);
-            else
-                t.template block<false>(j0, has, ka, va, false);
+                t.template block<true>(j0, has, k, v, special);
+        } else if (t.live) {
+            t.template block<false>(j0, has, k, v, false);
         }
+    };
+    for (int b = b0; b < b1; b += 2) {
+        step(b, ka, va, kb, vb);
+        if (b + 1 < b1)
+            step(b + 1, kb, vb, ka, va);
     }
 
     if (sh.np > 1) {
@@ -388,7 +405,7 @@ __device__ __forceinline__ void run_many(const AttnArgs &a, const Request &rq, i
             parts.put(st, t.m);
             parts.put(st + kWave, t.l);
         }
-        if (!last_part(a, sh, &lds_last))
+        if (!last_part(a, sh, t.thread, &lds_last))
             return;
         if (t.live) {
             t.m = kNegInf;
@@ -396,21 +413,33 @@ __device__ __forceinline__ void run_many(const AttnArgs &a, const Request &rq, i
 #pragma unroll
             for (int d = 0; d < DT; ++d)
                 t.o[d] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-            for (int i = 0; i < sh.np; ++i) {
-                const int from = sums(i), st = stats(i);
-                const float mi = parts.get(st), li = parts.get(st + kWave), next = fmaxf(t.m, mi);
-                const float f0 = t.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(t.m - next);
-                const float f1 = mi == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mi - next);
-                t.l = t.l * f0 + li * f1;
+            for (int i0 = 0; i0 < sh.np; i0 += 2) { // two at a time: a round trip to memory each
+                const int i1 = min(i0 + 1, sh.np - 1), from0 = sums(i0), from1 = sums(i1);
+                f32x4 x[2][4 * DT];
+                float m[2] = {parts.get(stats(i0)), parts.get(stats(i1))};
+                float l[2] = {parts.get(stats(i0) + kWave), parts.get(stats(i1) + kWave)};
+#pragma unroll
+                for (int e = 0; e < 4 * DT; ++e) {
+                    x[0][e] = parts.get4(from0 + e * (4 * kWave));
+                    x[1][e] = parts.get4(from1 + e * (4 * kWave));
+                }
+                if (i1 == i0) { // counted once
+                    m[1] = kNegInf;
+                    l[1] = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4 * DT; ++e)
+                        x[1][e] = f32x4{0, 0, 0, 0};
+                }
+                const float next = fmaxf(t.m, fmaxf(m[0], m[1]));
+                const float f = t.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(t.m - next);
+                const float f0 = m[0] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[0] - next);
+                const float f1 = m[1] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[1] - next);
+                t.l = t.l * f + l[0] * f0 + l[1] * f1;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const f32x4 x = parts.get4(from + (d * 4 + e) * (4 * kWave));
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            t.o[d][4 * e + c] = fmaf(x[c], f1, t.o[d][4 * e + c] * f0);
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        t.o[d][e] = fmaf(x[1][4 * d + e / 4][e % 4], f1, fmaf(x[0][4 * d + e / 4][e % 4], f0, t.o[d][e] * f));
                 t.m = next;
             }
         }

@@ -29,24 +29,31 @@ __device__ __forceinline__ uint32_t add_cut(uint32_t a, uint32_t b, uint32_t cap
     return s < cap ? s : cap;
 }
 
-// Exclusive prefix of v over a workgroup of WAVES waves; *total gets the whole
-// sum.  `scratch` holds WAVES words and is free again after the caller's next
-// barrier.
-template <int WAVES, class T, class Add>
-__device__ __forceinline__ T block_prefix(T v, T *scratch, T *total, Add add)
+// Another lane's value by a DPP control; 0 where the lane has no source.
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t dpp(uint32_t v)
 {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    T s = v;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const T o = __shfl_up(s, d);
-        if (lane >= d)
-            s = add(o, s);
-    }
+    return __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+
+// Exclusive prefix of v over a workgroup of WAVES waves; *total gets the whole
+// sum (add(0, v) is v).  `scratch` holds WAVES words and is free again after the
+// caller's next barrier.  Within a wave: shifts by 1, 2, 4 and 8 in rows of 16
+// lanes, then each row's last lane to the rows after it.
+template <int WAVES, class Add>
+__device__ __forceinline__ uint32_t block_prefix(int thread, uint32_t v, uint32_t *scratch, uint32_t *total, Add add)
+{
+    const int lane = thread & (kWave - 1), wave = thread / kWave;
+    uint32_t s = v;
+    s = add(dpp<0x111, 0xf>(s), s);
+    s = add(dpp<0x112, 0xf>(s), s);
+    s = add(dpp<0x114, 0xf>(s), s);
+    s = add(dpp<0x118, 0xf>(s), s);
+    s = add(dpp<0x142, 0xa>(s), s);
+    s = add(dpp<0x143, 0xc>(s), s);
     if (lane == kWave - 1)
         scratch[wave] = s;
     __syncthreads();
-    T base = 0, all = 0;
+    uint32_t base = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
         if (w == wave)
@@ -54,8 +61,7 @@ __device__ __forceinline__ T block_prefix(T v, T *scratch, T *total, Add add)
         all = add(all, scratch[w]);
     }
     *total = all;
-    const T before = __shfl_up(s, 1);
-    return lane == 0 ? base : add(base, before);
+    return add(base, dpp<0x138, 0xf>(s));
 }
 
 } // namespace

@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kThreads) void paged_slots_kernel(SlotsArgs a)
             f[i] = fr > 0 ? min((uint32_t)fr, (uint32_t)INT_MAX - c[i]) : 0;
             run = add_cut(run, min(f[i], tokens), tokens);
         }
-        uint32_t all, at = block_prefix<kThreads / kWave>(run, scratch, &all, cut);
+        uint32_t all, at = block_prefix<kThreads / kWave>(threadIdx.x, run, scratch, &all, cut);
         at = add_cut(tbase, at, tokens);
         const uint32_t tend = add_cut(tbase, all, tokens);
         uint32_t need = 0, p[kPer], s[kPer];
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kThreads) void paged_slots_kernel(SlotsArgs a)
             p[i] = need;
             need += pages_of(a.page, c[i] + f[i]) - pages_of(a.page, c[i]);
         }
-        const uint32_t pat = pbase + block_prefix<kThreads / kWave>(need, scratch + kThreads / kWave, &all, sum);
+        const uint32_t pat = pbase + block_prefix<kThreads / kWave>(threadIdx.x, need, scratch + kThreads / kWave, &all, sum);
         const uint32_t pend = pbase + all;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
