@@ -16,6 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgemv_fused.so")
+PY_SOURCE = os.path.join(CSRC, "paged", "paged_python.cpp")
+PY_LIB = os.path.join(HERE, "_paged_fast.so")
 PROBE_LIB = os.path.join(HERE, "libhbm_probe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -64,11 +66,31 @@ def build_cpu(verbose: bool = False) -> str:
     return CPU_LIB
 
 
+def build_python(verbose: bool = False) -> str:
+    """The CPython module that marshals the paged operators' tensors (host code)."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], INCLUDE]
+    lib = os.path.join(root, "lib")
+    tmp = PY_LIB + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(f for i in include for f in ("-isystem", i)), "-o", tmp, PY_SOURCE, "-L", lib, "-ltorch_python", "-ltorch_cpu",
+          "-lc10"], verbose)
+    os.replace(tmp, PY_LIB)
+    return PY_LIB
+
+
 def build(verbose: bool = False) -> str:
-    """Builds the GEMV library, the benchmark's measurement library and the
-    CPU comparison GEMV."""
+    """Builds the GEMV library, the benchmark's measurement library, the CPU
+    comparison GEMV and the paged operators' Python module."""
     _compile(PROBE_SOURCES, PROBE_LIB, verbose)
     build_cpu(verbose)
+    build_python(verbose)
     return _compile(SOURCES, LIB, verbose)
 
 

@@ -9,6 +9,10 @@ Launches go to ``stream`` (default: torch's current stream); as with any
 launch outside torch, a tensor used on another stream than the one it was
 made on has to be kept alive, or recorded on that stream, by the caller.
 
+Calls go through ``_paged_fast`` first (C++, 1 us a call where the same checks
+here take 6); what it does not take at once comes to the checks below, which
+accept the call or raise.
+
 A cache is a pair of tensors ``[pages, page_size, heads, dim]`` of float16 or
 bfloat16 with any strides whose innermost is 1 (a ``[pages, heads, page_size,
 dim]`` buffer goes in as ``buffer.transpose(1, 2)``).
@@ -30,11 +34,13 @@ class GemvKvCache(ctypes.Structure):
 
 _CACHEP = ctypes.POINTER(GemvKvCache)
 _LIB = None
+_FAST = None      # the module that checks and marshals a call's tensors at once
+_DEVICE = None    # () -> index of the current GPU, -1 if there is none
 
 
 def load():
     """The library, with the paged operators declared; torch's types are known after it."""
-    global _LIB, TYPES
+    global _LIB, _FAST, _DEVICE, TYPES
     if _LIB is not None:
         return _LIB
     import torch
@@ -51,6 +57,15 @@ def load():
     lib.gemv_paged_attn_workspace.argtypes = [_I64]
     lib.gemv_paged_attn_workspace.restype = _I64
     TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    try:
+        from . import _paged_fast
+    except ImportError as e:
+        raise ImportError(f"{e}; build it with: python -m decode_gemv_elementwise_amd.build") from e
+    _paged_fast.bind(*(ctypes.cast(getattr(lib, f), _VP).value
+                       for f in ("gemv_paged_slots", "gemv_paged_append", "gemv_paged_attn")))
+    _FAST = _paged_fast
+    raw = getattr(torch._C, "_cuda_getDevice", None)
+    _DEVICE = (raw or torch.cuda.current_device) if torch.cuda.is_available() else lambda: -1
     _LIB = lib
     return lib
 
@@ -134,8 +149,16 @@ def gemv_paged_slots(cached, fresh, free_pages, page_size, block_table, query_st
     """Block tables and slot maps of a step from its requests' lengths: ``cached`` and ``fresh`` [requests] in;
     ``block_table`` [requests, width] extended by pages of ``free_pages``; ``query_start`` [requests + 1], ``kv_len``
     [requests], ``token_request``, ``positions`` and ``slots`` [tokens] and ``used`` [1] out, all int32."""
-    import torch
     lib = _LIB or load()
+    device = _DEVICE()
+    if device >= 0:
+        st = _FAST.slots(cached, fresh, free_pages, page_size, block_table, query_start, kv_len, token_request, positions,
+                         slots, used, device, binding._stream(stream))
+        if st == 0:
+            return
+        if st is not None:
+            binding._raise(st)
+    import torch
     i32 = torch.int32
     dev = _device_of(cached, "cached")
     n, tokens = cached.numel(), slots.numel()
@@ -156,8 +179,16 @@ def gemv_paged_append(q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cac
     """Rotary positions for q [tokens, q_heads, dim] and k [tokens, heads, dim] (float32, float16 or bfloat16 rows, any
     row stride), q into ``q_out`` and k and v into the cache at ``slots`` [tokens].  ``positions`` is [tokens] or
     [axes, tokens] int32, ``inv_freq`` [rot / 2] float32, ``axis`` [rot / 2] int32 the axis of each pair."""
-    import torch
     lib = _LIB or load()
+    device = _DEVICE()
+    if device >= 0:
+        st = _FAST.append(q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache, axis, STYLES.get(style, style),
+                          device, binding._stream(stream))
+        if st == 0:
+            return
+        if st is not None:
+            binding._raise(st)
+    import torch
     i32 = torch.int32
     dev = _device_of(q, "q")
     if q.dim() != 3 or q.dtype not in TYPES:
@@ -189,8 +220,16 @@ def gemv_paged_attn(q, k_cache, v_cache, block_table, query_start, kv_len, scale
     dst alike (or float32), both with any token and head strides; ``block_table`` [requests, width], ``query_start``
     [requests + 1], ``kv_len`` [requests] int32; ``window`` > 0 limits a token to the last ``window`` keys and the first
     ``sinks``.  ``workspace`` (see ``attn_workspace``) lets the keys of few rows be split over the whole card."""
-    import torch
     lib = _LIB or load()
+    device = _DEVICE()
+    if device >= 0:
+        st = _FAST.attn(q, k_cache, v_cache, block_table, query_start, kv_len, scale, dst, workspace, window, sinks, device,
+                        binding._stream(stream))
+        if st == 0:
+            return
+        if st is not None:
+            binding._raise(st)
+    import torch
     dev = _device_of(q, "q")
     cache = _cache_of(k_cache, v_cache, dev)
     if q.dim() != 3 or q.dtype != k_cache.dtype or q.shape[2] != cache.dim:
