@@ -27,11 +27,12 @@
 namespace gemv {
 namespace {
 
-constexpr int kFewShare = 8;   // blocks of 32 keys that a workgroup takes at least
-constexpr int kManyShare = 8;  // the same where any tile has many rows
-// A share's end this near a tile's edge moves to it: starting on a tile, and
-// joining its parts, cost about as much as so many blocks.
-constexpr uint32_t kFewEdge = 8, kManyEdge = 12;
+// In blocks of 32 keys: what a workgroup takes at least, and how near a tile's edge
+// a share's end moves to it.  Starting on a tile, and joining its parts, cost about
+// as much as the blocks of `edge`; a block's own time goes by the heads' width.
+constexpr uint32_t least_share(int dim) { return 1024 / dim; }
+constexpr uint32_t few_edge(int dim) { return 1024 / dim; }
+constexpr uint32_t many_edge(int dim) { return 1536 / dim; }
 constexpr uint32_t kMostCost = INT_MAX;
 
 __device__ __forceinline__ bool is_few(const AttnArgs &a, const Request &q) { return (int64_t)q.n * a.group <= kFewRows; }
@@ -65,7 +66,7 @@ __device__ __forceinline__ const AttnArgs &arguments()
     return *(const AttnArgs *)p;
 }
 
-template <bool BF, int D, bool F32OUT, bool PAGE8>
+template <bool BF, int D, bool F32OUT, int PAGES>
 __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(AttnArgs)
 {
     const AttnArgs &a = arguments();
@@ -128,8 +129,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(AttnArgs)
                 total = here;
                 many = any;
             }
-            const uint32_t share = many ? kManyShare : kFewShare;
-            const uint32_t groups = uniform(min(gridDim.x, (total + share - 1) / share));
+            const uint32_t groups = uniform(min(gridDim.x, (total + least_share(D) - 1) / least_share(D)));
             if (w >= groups || total == kMostCost)
                 return;
             each = uniform(total / groups);
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(AttnArgs)
             x1 = x + each + (w < more);
             // a tile is cut only if the parts have room: two for each workgroup, below 2^28 floats in all
             stride = many ? many_part(D) : few_part(D);
-            edge = a.part_room < 2 * (int64_t)groups * stride ? kMostCost / 2 : many ? kManyEdge : kFewEdge;
+            edge = a.part_room < 2 * (int64_t)groups * stride ? kMostCost / 2 : many ? many_edge(D) : few_edge(D);
         }
         while (x < x1 && x < base + here) {
             int lo = 0, hi = min(kThreads, a.requests - r0);
@@ -173,11 +173,11 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(AttnArgs)
             }
             const int head = uniform(unit / tiles), tile = unit - head * tiles;
             if (is_few(a, q))
-                run_few<BF, D, F32OUT, PAGE8>(arguments(), q, r0 + lo, head, sh, reinterpret_cast<float *>(ka),
+                run_few<BF, D, F32OUT, PAGES>(arguments(), q, r0 + lo, head, sh, reinterpret_cast<float *>(ka),
                                               reinterpret_cast<float *>(va), reinterpret_cast<float *>(kb),
                                               reinterpret_cast<float *>(vb));
             else
-                run_many<BF, D, F32OUT, PAGE8>(arguments(), q, r0 + lo, tile, head, sh, ka, va, kb, vb);
+                run_many<BF, D, F32OUT, PAGES>(arguments(), q, r0 + lo, tile, head, sh, ka, va, kb, vb);
         }
         if (x >= x1)
             return;
@@ -186,18 +186,18 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(AttnArgs)
     }
 }
 
-template <bool BF, int D> const void *kernel_of(bool f32out, bool page8)
+template <bool BF, int D, bool F32OUT> const void *kernel_of(int pages)
 {
-    if (f32out)
-        return page8 ? reinterpret_cast<const void *>(&paged_attn_kernel<BF, D, true, true>)
-                     : reinterpret_cast<const void *>(&paged_attn_kernel<BF, D, true, false>);
-    return page8 ? reinterpret_cast<const void *>(&paged_attn_kernel<BF, D, false, true>)
-                 : reinterpret_cast<const void *>(&paged_attn_kernel<BF, D, false, false>);
+    return pages == 16  ? reinterpret_cast<const void *>(&paged_attn_kernel<BF, D, F32OUT, 16>)
+           : pages == 8 ? reinterpret_cast<const void *>(&paged_attn_kernel<BF, D, F32OUT, 8>)
+                        : reinterpret_cast<const void *>(&paged_attn_kernel<BF, D, F32OUT, 0>);
 }
 
-template <int D> const void *kernel_of(int type, bool f32out, bool page8)
+template <int D> const void *kernel_of(int type, bool f32out, int pages)
 {
-    return type == GEMV_W_BF16 ? kernel_of<true, D>(f32out, page8) : kernel_of<false, D>(f32out, page8);
+    if (type == GEMV_W_BF16)
+        return f32out ? kernel_of<true, D, true>(pages) : kernel_of<true, D, false>(pages);
+    return f32out ? kernel_of<false, D, true>(pages) : kernel_of<false, D, false>(pages);
 }
 
 } // namespace
@@ -223,7 +223,7 @@ extern "C" int gemv_paged_attn(const void *q, int64_t q_token_stride, int64_t q_
     a.v = static_cast<const uint16_t *>(cache->v);
     a.q_ts = q_token_stride, a.q_hs = q_head_stride, a.o_ts = out_token_stride, a.o_hs = out_head_stride;
     for (int d = 0; d < 3; ++d)
-        a.k_stride[d] = cache->k_stride[d], a.v_stride[d] = cache->v_stride[d];
+        a.k_stride[d] = (uint32_t)cache->k_stride[d], a.v_stride[d] = (uint32_t)cache->v_stride[d];
     a.table = block_table, a.query_start = query_start, a.kv_len = kv_len, a.table_stride = table_stride;
     a.out = out;
     const int64_t room = (workspace_bytes - gemv::kAttnCounters * 4) / 4;
@@ -241,10 +241,13 @@ extern "C" int gemv_paged_attn(const void *q, int64_t q_token_stride, int64_t q_
     a.q_flip = scale < 0.0f && s != 0.0f ? 0x80008000u : 0u;
     a.page = gemv::fast_div(cache->page_size), a.per_group = gemv::fast_div(a.group);
 
-    const bool f32out = out_type == GEMV_W_F32, page8 = cache->page_size % 8 == 0;
-    const void *fn = cache->dim == 64    ? gemv::kernel_of<64>(cache->type, f32out, page8)
-                     : cache->dim == 128 ? gemv::kernel_of<128>(cache->type, f32out, page8)
-                                         : gemv::kernel_of<256>(cache->type, f32out, page8);
+    const bool f32out = out_type == GEMV_W_F32;
+    // runs of keys that lie in one page; copies of 16 take 32-bit offsets within a run
+    const bool near = a.k_stride[1] < (1u << 27) && a.v_stride[1] < (1u << 27);
+    const int pages = cache->page_size % 16 == 0 && near ? 16 : cache->page_size % 8 == 0 ? 8 : 0;
+    const void *fn = cache->dim == 64    ? gemv::kernel_of<64>(cache->type, f32out, pages)
+                     : cache->dim == 128 ? gemv::kernel_of<128>(cache->type, f32out, pages)
+                                         : gemv::kernel_of<256>(cache->type, f32out, pages);
     // no more workgroups than shares can be: row tiles times the blocks that the
     // table's width allows
     const int64_t blocks = (a.reach + gemv::kFewBlock - 1) / gemv::kFewBlock;
@@ -254,7 +257,7 @@ extern "C" int gemv_paged_attn(const void *q, int64_t q_token_stride, int64_t q_
            (blocks + (1ll << a.unit_log2) - 1) >> a.unit_log2 > (INT_MAX - 1) / tiles)
         ++a.unit_log2;
     const int64_t most = gemv::kAttnGroups;
-    const int64_t shares = (blocks + gemv::kFewShare - 1) / gemv::kFewShare;
+    const int64_t shares = (blocks + gemv::least_share(256) - 1) / gemv::least_share(256);
     const int grid = (int)(tiles >= most || shares >= most || tiles * shares >= most ? most : tiles * shares);
     void *args[] = {&a};
     const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)grid), dim3(gemv::kThreads), args, 0,

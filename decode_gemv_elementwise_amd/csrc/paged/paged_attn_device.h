@@ -22,7 +22,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct AttnArgs {
     const uint16_t *q, *k, *v;
-    int64_t q_ts, q_hs, k_stride[3], v_stride[3], o_ts, o_hs;
+    int64_t q_ts, q_hs, o_ts, o_hs;
+    uint32_t k_stride[3], v_stride[3]; // below 2^31
     const int32_t *table, *query_start, *kv_len;
     int64_t table_stride;
     void *out;
@@ -95,6 +96,20 @@ template <bool BF> __device__ __forceinline__ u32x4 round8(const float *p, float
         rest[i] = p[i] - (float)r[i];
     }
     return __builtin_bit_cast(u32x4, r);
+}
+
+// Two floats rounded to nearest into 16 bits; p gets what each lost.
+template <bool BF> __device__ __forceinline__ uint32_t round2(float *p)
+{
+    typedef typename std::conditional<BF, __bf16, _Float16>::type T;
+    typedef T t2 __attribute__((ext_vector_type(2)));
+    t2 r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r[i] = (T)p[i];
+        p[i] -= (float)r[i];
+    }
+    return __builtin_bit_cast(uint32_t, r);
 }
 
 template <bool BF> __device__ __forceinline__ float as_float(uint16_t x)
@@ -171,27 +186,40 @@ __device__ __forceinline__ bool sees_all(const AttnArgs &a, int p_lo, int p_hi, 
     return j0 + n - 1 <= p_lo && (a.window == 0 || j0 > p_hi - a.window || j0 + n <= a.sinks);
 }
 
-// The page id of key j as the table has it, -1 past the table's end; and -1 for
-// one that is no page.
-__device__ __forceinline__ int raw_id(const AttnArgs &a, const int32_t *table, int j)
+// A scalar the compiler may not read again from the arguments: in a loop over keys
+// that would be waited for at every block.
+template <class T> __device__ __forceinline__ T kept(T x)
 {
-    const uint32_t at = div_by(a.page, j);
-    return at < (uint32_t)a.width ? table[at] : -1;
+    asm volatile("" : "+s"(x));
+    return x;
 }
 
-__device__ __forceinline__ int checked_id(const AttnArgs &a, int id) { return (unsigned)id < (unsigned)a.num_pages ? id : -1; }
+// What finds a key in the cache.
+struct Paging {
+    FastDiv page;
+    uint32_t width, pages, k0, k1, v0, v1; // strides of page and of token in page
 
-__device__ __forceinline__ int id_of(const AttnArgs &a, const int32_t *table, int j)
-{
-    return checked_id(a, raw_id(a, table, j));
-}
+    // The page id of key j as the table has it, -1 past the table's end.
+    __device__ __forceinline__ int raw(const int32_t *table, int j) const
+    {
+        const uint32_t at = div_by(page, j);
+        return at < width ? table[at] : -1;
+    }
+    // -1 for what is no page.
+    __device__ __forceinline__ int checked(int id) const { return (uint32_t)id < pages ? id : -1; }
+    // Element offset of key j in page id (a key without a page reads page 0, and
+    // what is read is dropped).
+    template <bool V> __device__ __forceinline__ uint64_t offset(int id, int j) const
+    {
+        const uint32_t in = j - div_by(page, j) * page.d;
+        return (uint64_t)(uint32_t)max(id, 0) * (V ? v0 : k0) + (uint64_t)in * (V ? v1 : k1);
+    }
+};
 
-// Element offset of key j in page id (a key without a page reads page 0, and
-// what is read is dropped).
-__device__ __forceinline__ int64_t key_offset(const AttnArgs &a, const int64_t *stride, int id, int j)
+__device__ __forceinline__ Paging paging_of(const AttnArgs &a)
 {
-    const uint32_t in = j - div_by(a.page, j) * a.page.d;
-    return (int64_t)max(id, 0) * stride[0] + (int64_t)in * stride[1];
+    return Paging{{kept(a.page.mul), kept(a.page.shift), kept(a.page.d)}, kept((uint32_t)a.width), kept((uint32_t)a.num_pages),
+                  kept(a.k_stride[0]), kept(a.k_stride[1]), kept(a.v_stride[0]), kept(a.v_stride[1])};
 }
 
 // A workgroup's share of the keys of one row tile: of np workgroups it is the

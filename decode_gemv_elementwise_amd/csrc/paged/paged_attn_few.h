@@ -36,7 +36,8 @@ __device__ __forceinline__ float row_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
+template <bool BF, int D, bool F32OUT, int PAGES> struct FewRows {
+    static constexpr bool PAGE8 = PAGES != 0; // eight keys from a multiple of eight on lie in one page
     static constexpr int KS = D / 32;    // k steps of the first product
     static constexpr int VPL = D / 16;   // values of a v row in a lane
     static constexpr int VW = VPL / 2;   // the same in words
@@ -49,7 +50,8 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
     int lane, col, grp;
     u32x4 qf[KS];
     f32x4 o[VPL];
-    float m, l;
+    float m, l, scale;
+    Paging paging;
 
     __device__ FewRows(const AttnArgs &args) : a(args) {}
 
@@ -61,9 +63,11 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
         const int rows = rq.n * a.group, row = col;
         p_lo = rq.kv - rq.n;
         p_hi = rq.kv - 1;
-        kbase = a.k + head * a.k_stride[2];
-        vbase = a.v + head * a.v_stride[2];
+        kbase = a.k + (int64_t)head * a.k_stride[2];
+        vbase = a.v + (int64_t)head * a.v_stride[2];
         table = a.table + r * a.table_stride;
+        paging = paging_of(a);
+        scale = kept(a.scale_log2);
         p_row = -1;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
@@ -103,10 +107,10 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
     {
 #pragma unroll
         for (int i = 0; i < NK; ++i)
-            ids.k[i] = raw_id(a, table, krun(j0) + 4 * i);
+            ids.k[i] = paging.raw(table, krun(j0) + 4 * i);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            ids.v[i] = raw_id(a, table, vrun(j0) + i);
+            ids.v[i] = paging.raw(table, vrun(j0) + i);
     }
 
     // Asks for a block's k and v.
@@ -114,21 +118,21 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
     {
         const uint16_t *kp = kbase + 8 * grp, *vp = vbase + VPL * col;
         if constexpr (PAGE8) { // a run of eight lies in one page
-            kp += key_offset(a, a.k_stride, checked_id(a, ids.k[0]), krun(j0));
-            vp += key_offset(a, a.v_stride, checked_id(a, ids.v[0]), vrun(j0));
+            kp += paging.template offset<false>(paging.checked(ids.k[0]), krun(j0));
+            vp += paging.template offset<true>(paging.checked(ids.v[0]), vrun(j0));
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint16_t *src = PAGE8 ? kp + 4 * i * a.k_stride[1]
-                                        : kp + key_offset(a, a.k_stride, checked_id(a, ids.k[PAGE8 ? 0 : i]), krun(j0) + 4 * i);
+            const uint16_t *src = PAGE8 ? kp + 4ull * i * paging.k1
+                                        : kp + paging.template offset<false>(paging.checked(ids.k[PAGE8 ? 0 : i]), krun(j0) + 4 * i);
 #pragma unroll
             for (int s = 0; s < KS; ++s)
                 x.k[i][s] = *reinterpret_cast<const u32x4 *>(src + 32 * s);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint16_t *src = PAGE8 ? vp + i * a.v_stride[1]
-                                        : vp + key_offset(a, a.v_stride, checked_id(a, ids.v[PAGE8 ? 0 : i]), vrun(j0) + i);
+            const uint16_t *src = PAGE8 ? vp + (uint64_t)i * paging.v1
+                                        : vp + paging.template offset<true>(paging.checked(ids.v[PAGE8 ? 0 : i]), vrun(j0) + i);
             if constexpr (VW == 2) {
                 const u32x2 y = *reinterpret_cast<const u32x2 *>(src);
                 x.v[i][0] = y[0];
@@ -146,7 +150,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
         x.has = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            x.has |= (uint32_t)(checked_id(a, ids.v[PAGE8 ? 0 : i]) >= 0) << i;
+            x.has |= (uint32_t)(paging.checked(ids.v[PAGE8 ? 0 : i]) >= 0) << i;
         __builtin_amdgcn_sched_barrier(0); // all are asked for before anything waits for one
     }
 
@@ -162,8 +166,8 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[i] = s0[i] * a.scale_log2;
-                p[4 + i] = s1[i] * a.scale_log2;
+                p[i] = s0[i] * scale;
+                p[4 + i] = s1[i] * scale;
             }
         }
         // every row of the tile sees every key of the block
@@ -245,11 +249,11 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
         for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int j = j0 + 8 * g + i, id = id_of(a, table, j);
+                const int j = j0 + 8 * g + i, id = paging.checked(paging.raw(table, j));
                 const float w = __shfl(p[i], 16 * g + col);
                 if (id < 0 || !sees(a, p_row, j))
                     continue;
-                const uint16_t *src = vbase + key_offset(a, a.v_stride, id, j) + 4 * VPL * grp;
+                const uint16_t *src = vbase + paging.template offset<true>(id, j) + 4 * VPL * grp;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -264,7 +268,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct FewRows {
 
 // A share of a row tile's keys.  lds0 to lds3: one a wave, of at least 16 (D + 4)
 // floats each; they are free again on return.
-template <bool BF, int D, bool F32OUT, bool PAGE8>
+template <bool BF, int D, bool F32OUT, int PAGES>
 __device__ __forceinline__ void run_few(const AttnArgs &a, const Request &rq, int r, int head, const Share &sh,
                                         float *lds0, float *lds1, float *lds2, float *lds3)
 {
@@ -273,7 +277,7 @@ __device__ __forceinline__ void run_few(const AttnArgs &a, const Request &rq, in
     __shared__ int lds_last;
     const int thread = thread_here(), wave = uniform(thread / kWave);
 
-    FewRows<BF, D, F32OUT, PAGE8> t(a);
+    FewRows<BF, D, F32OUT, PAGES> t(a);
     t.begin(rq, r, head, thread);
     const Walk walk = walk_of<kFewBlock>(a, t.p_lo, t.p_hi);
     // shares begin at whole rounds of the waves

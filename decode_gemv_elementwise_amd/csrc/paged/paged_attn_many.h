@@ -11,8 +11,11 @@
 // LDS in that order, turned on the way by the transposing 64-bit LDS read (4 keys
 // by 16 values to 16 lanes).
 //
-// Memory to LDS goes without registers, 16 bytes a lane, one block ahead of the
-// products: two buffers for k and two for v, one barrier a block.  A row of
+// A wave forms a block's weights while the matrix core forms the next block's
+// scores: exponentials and products then share the time instead of adding up.
+//
+// Memory to LDS goes without registers, 16 bytes a lane, ahead of the products:
+// two buffers for k and two for v, one barrier a block.  A row of
 // D values lies in one piece; which 16-byte chunk of it a lane fetches is
 // permuted by the row, so that the products' reads meet no bank twice (k_turn,
 // v_turn).
@@ -56,14 +59,15 @@ __device__ __forceinline__ float half_sum(float v)
     return __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
 }
 
-template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
+template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
     static constexpr int kBlock = many_block(D), KT = kBlock / 32; // keys of a block; tiles of 32 of them
     static constexpr int kRowBytes = 2 * D, kChunks = D / 8;      // 16-byte chunks of a row
     static constexpr int kRun = kWave / kChunks;                  // rows that one wave instruction brings
     static constexpr int kFetch = kBlock / (kRun * kWaves);   // such instructions of a wave per block
+    static constexpr int kOwn = kBlock / kWaves;                  // rows, next to each other, that a wave brings
     static constexpr int KS = D / 16;                             // k steps of the first product
     static constexpr int kHalves = many_halves(D), DW = D / kHalves, DT = DW / 32; // values of a wave, tiles of them
-    static constexpr int kAhead = 2; // products between a read of LDS and its use
+    static constexpr int kAhead = 2, kVAhead = 2; // products between a read of LDS and its use
     // binary16's weights are lifted, which leaves one power of two to its largest
     static constexpr float kSlack = BF ? 8.0f : 1.0f;
 
@@ -75,7 +79,9 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
     bool live;                 // the wave has rows
     int thread, lane, wave, col, half;
     int values; // first of the wave's values
-    int64_t k_lane, v_lane; // byte offset of the lane's row within a run
+    uint32_t k_piece, v_piece; // byte of a row at which the lane's piece of the wave's first run lies
+    Paging paging;
+    float scale;
     u32x4 qf[KS];
     f32x16 o[DT];
     float m, l;
@@ -108,12 +114,13 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
         live = wrow < rows;
         w_lo = before + (int)div_by(a.per_group, min(wrow, rows - 1));
         w_hi = before + (int)div_by(a.per_group, min(wrow + 32, rows) - 1);
-        kbase = reinterpret_cast<const char *>(a.k + head * a.k_stride[2]);
-        vbase = reinterpret_cast<const char *>(a.v + head * a.v_stride[2]);
+        kbase = reinterpret_cast<const char *>(a.k + (int64_t)head * a.k_stride[2]);
+        vbase = reinterpret_cast<const char *>(a.v + (int64_t)head * a.v_stride[2]);
         table = a.table + r * a.table_stride;
-        k_lane = 2 * (lane / kChunks) * a.k_stride[1];
-        v_lane = 2 * (lane / kChunks) * a.v_stride[1];
-        asm volatile("" : "+v"(k_lane), "+v"(v_lane)); // kept as they are: the rest of an address is the wave's
+        paging = paging_of(a);
+        scale = kept(a.scale_log2);
+        k_piece = 16 * (lane % kChunks ^ k_turn(wave * kOwn + lane / kChunks));
+        v_piece = 16 * (lane % kChunks ^ v_turn(wave * kOwn + lane / kChunks));
         p_row = -1;
         const int row = wrow + col;
         const int i = div_by(a.per_group, min(row, rows - 1)), g = min(row, rows - 1) - i * a.group;
@@ -131,26 +138,27 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
             o[i] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     }
 
-    // Starts the copy of block j0 into LDS; ids: the page of each lane's key.
-    __device__ __forceinline__ void fetch(int j0, int ids, char *k, char *v) const
+    // Starts the copy of block j0 of k (or v) into LDS; ids: the page of each lane's key.
+    template <bool V> __device__ __forceinline__ void fetch(int j0, int ids, char *to) const
     {
-        const int r = lane / kChunks, phys = lane % kChunks;
+        const int own = wave * kOwn, r = lane / kChunks;
+        const char *base = V ? vbase : kbase;
+        const uint32_t piece = V ? v_piece : k_piece, step = 2 * (V ? paging.v1 : paging.k1);
+        if constexpr (PAGES == 16) // a wave's rows lie in one page
+            base += 2 * paging.template offset<V>(__builtin_amdgcn_readlane(ids, own), j0 + own);
 #pragma unroll
         for (int f = 0; f < kFetch; ++f) {
-            const int row0 = (f * kWaves + wave) * kRun, row = row0 + r;
-            const int kc = 16 * (phys ^ k_turn(row)), vc = 16 * (phys ^ v_turn(row));
-            const char *kp, *vp;
-            if constexpr (PAGE8) { // a run lies in one page
-                const int id = __builtin_amdgcn_readlane(ids, row0);
-                kp = kbase + 2 * key_offset(a, a.k_stride, id, j0 + row0) + k_lane;
-                vp = vbase + 2 * key_offset(a, a.v_stride, id, j0 + row0) + v_lane;
+            // the turns of rows own + r and f kRun have no bits in common: together they are the row's
+            const uint32_t at = piece ^ (16 * (V ? v_turn(f * kRun) : k_turn(f * kRun)));
+            const char *from;
+            if constexpr (PAGES == 16) {
+                from = base + (r * step + at);
+                base += (uint64_t)kRun * step;
             } else {
-                const int id = __shfl(ids, row);
-                kp = kbase + 2 * key_offset(a, a.k_stride, id, j0 + row);
-                vp = vbase + 2 * key_offset(a, a.v_stride, id, j0 + row);
+                const int row = own + f * kRun + r;
+                from = base + 2 * paging.template offset<V>(__shfl(ids, row), j0 + row) + at;
             }
-            __builtin_amdgcn_global_load_lds((global_void *)(kp + kc), (lds_void *)(k + row0 * kRowBytes), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((global_void *)(vp + vc), (lds_void *)(v + row0 * kRowBytes), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)(to + (own + f * kRun) * kRowBytes), 16, 0, 0);
         }
     }
 
@@ -191,39 +199,81 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
         return seen;
     }
 
-    // One block of keys; part: some rows do not see some of its keys.
-    template <bool PART> __device__ __forceinline__ void block(int j0, uint64_t has, const char *k, const char *v, bool special)
+    // This lane's words of a block of k for the first product's n-th step, and of v
+    // for the second's.
+    struct KAt {
+        const char *k;
+        int row, turn;
+        __device__ __forceinline__ KAt(const char *k, int ln)
+            : k(k), row((ln & 31) * kRowBytes), turn(16 * ((ln >> 5) ^ k_turn(ln & 31)))
+        {
+        }
+        __device__ __forceinline__ u32x4 operator()(int n) const // rows 32 apart have the same turn
+        {
+            return *reinterpret_cast<const u32x4 *>(k + (row + (turn ^ (32 * (n / KT)))) + n % KT * 32 * kRowBytes);
+        }
+    };
+    struct VAt {
+        const char *v;
+        int row, turn;
+        // 16 lanes bring 4 keys by 16 values
+        __device__ __forceinline__ VAt(const char *v, int ln, int values) : v(v)
+        {
+            const int key = 4 * (ln >> 5) + ((ln & 15) >> 2), chunk = 2 * ((ln >> 4) & 1) + ((ln & 3) >> 1);
+            row = key * kRowBytes + 2 * values + 8 * (ln & 1);
+            turn = 16 * (chunk ^ v_turn(key));
+        }
+        __device__ __forceinline__ u32x4 operator()(int n) const // rows 8 apart have the same turn
+        {
+            const char *at = v + (row + (turn ^ (64 * (n % DT))));
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 16 * (n / DT) * kRowBytes));
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + (16 * (n / DT) + 8) * kRowBytes));
+            const u32x2 lo = __builtin_bit_cast(u32x2, x), hi = __builtin_bit_cast(u32x2, y);
+            return u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+    };
+
+    // The lane as the compiler knows no other: places in LDS are formed where they
+    // are used; all of them at once, for all buffers, would not leave registers enough.
+    __device__ __forceinline__ int lane_here() const
     {
-        // places in LDS are formed here each time: all of them at once, for both
-        // buffers, would not leave registers enough
         int ln = lane;
         asm volatile("" : "+v"(ln));
-        f32x16 s[KT];
-        {
-            const int row = (ln & 31) * kRowBytes;
-            const int turn = 16 * ((ln >> 5) ^ k_turn(ln & 31));
+        return ln;
+    }
+
+    // The scores of a block of keys, with `between(n)` after the n-th of its N
+    // products: work of other registers that the matrix core does not wait for.
+    // The order is kept as written: left alone, the compiler waits for each read.
+    template <class F> __device__ __forceinline__ void scores(const char *k, f32x16 *s, F between) const
+    {
+        constexpr int N = KS * KT;
+        const KAt at(k, lane_here());
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
-                s[t] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-            // rows 32 apart have the same turn
-            const auto read = [&](int n) {
-                return *reinterpret_cast<const u32x4 *>(k + (row + n % KT * 32 * kRowBytes + (turn ^ (32 * (n / KT)))));
-            };
-            u32x4 f[kAhead];
+        for (int t = 0; t < KT; ++t)
+            s[t] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        u32x4 f[kAhead];
 #pragma unroll
-            for (int n = 0; n < kAhead; ++n)
-                f[n] = read(n);
-            // the order is kept: left alone, the compiler waits for each read in turn
+        for (int n = 0; n < kAhead; ++n)
+            f[n] = at(n);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            s[n % KT] = mfma32<BF>(f[n % kAhead], qf[n / KT], s[n % KT]);
+            if (n + kAhead < N)
+                f[n % kAhead] = at(n + kAhead);
+            between(n);
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int n = 0; n < KS * KT; ++n) {
-                s[n % KT] = mfma32<BF>(f[n % kAhead], qf[n / KT], s[n % KT]);
-                if (n + kAhead < KS * KT)
-                    f[n % kAhead] = read(n + kAhead);
-                __builtin_amdgcn_sched_barrier(0);
-            }
         }
-        if constexpr (PART) {
+    }
+
+    // One block of keys whose scores are in s: their weights, formed while the
+    // products of the next block (k there) run into `next`, then the sums over v.
+    // part: some rows do not see some of its keys.
+    __device__ __forceinline__ void block(int j0, uint64_t has, const char *k, const char *v, bool part, bool special,
+                                          f32x16 *s, f32x16 *next)
+    {
+        if (part) {
             // by masks of all bits, not by comparisons: 32 of those would take 64 scalar registers
             const uint64_t seen = seen_of(j0, has) >> (4 * half);
 #pragma unroll
@@ -243,7 +293,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 top = fmaxf(top, s[t][i]);
-        top = half_max(top) * a.scale_log2;
+        top = half_max(top) * scale;
         if (__any(top > m + kSlack)) {
             const float to = fmaxf(m, top);
             const float f = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
@@ -254,51 +304,42 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
             m = to;
         }
         const float base = m == kNegInf ? 0.0f : BF ? m : m - kF16Lift;
-        u32x4 pf[2 * KT], pl[F32OUT ? 2 * KT : 1];
+        u32x4 pf[2 * KT], pl[F32OUT ? 2 * KT : 1]; // the weights in pairs, and what their rounding lost
+        scores(k, next, [&](int n) {
+            constexpr int N = KS * KT, kPairs = 8 * KT;
 #pragma unroll
-        for (int t = 0; t < 2 * KT; ++t) {
-            float p[8], rest[8];
+            for (int e = n * kPairs / N; e < (n + 1) * kPairs / N; ++e) {
+                float p[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(fmaf(s[t / 2][8 * (t & 1) + i], a.scale_log2, -base));
-                l += p[i];
+                for (int i = 0; i < 2; ++i) {
+                    p[i] = __builtin_amdgcn_exp2f(fmaf(s[e / 8][2 * e % 16 + i], scale, -base));
+                    l += p[i];
+                }
+                pf[e / 4][e % 4] = round2<BF>(p);
+                if constexpr (F32OUT)
+                    pl[e / 4][e % 4] = round2<BF>(p);
             }
-            pf[t] = round8<BF>(p, rest);
-            if constexpr (F32OUT) {
-                float none[8];
-                pl[t] = round8<BF>(rest, none);
-            }
-        }
+        });
         {
-            // 16 lanes bring 4 keys by 16 values
-            const int key = 4 * (ln >> 5) + ((ln & 15) >> 2), chunk = 2 * ((ln >> 4) & 1) + ((ln & 3) >> 1);
-            const int row = key * kRowBytes + 2 * values + 8 * (ln & 1);
-            const int turn = 16 * (chunk ^ v_turn(key));
-            const auto read = [&](int n) { // rows 8 apart have the same turn
-                const int at = row + 16 * (n / DT) * kRowBytes + (turn ^ (64 * (n % DT)));
-                const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(v + at));
-                const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(v + (at + 8 * kRowBytes)));
-                const u32x2 lo = __builtin_bit_cast(u32x2, x), hi = __builtin_bit_cast(u32x2, y);
-                return u32x4{lo[0], lo[1], hi[0], hi[1]};
-            };
-            u32x4 f[kAhead];
+            constexpr int N = 2 * KT * DT;
+            const VAt at(v, lane_here(), values);
+            u32x4 f[kVAhead];
 #pragma unroll
-            for (int n = 0; n < kAhead; ++n)
-                f[n] = read(n);
+            for (int n = 0; n < kVAhead; ++n)
+                f[n] = at(n);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int n = 0; n < 2 * KT * DT; ++n) {
-                o[n % DT] = mfma32<BF>(f[n % kAhead], pf[n / DT], o[n % DT]);
+            for (int n = 0; n < N; ++n) {
+                o[n % DT] = mfma32<BF>(f[n % kVAhead], pf[n / DT], o[n % DT]);
                 if constexpr (F32OUT)
-                    o[n % DT] = mfma32<BF>(f[n % kAhead], pl[n / DT], o[n % DT]);
-                if (n + kAhead < 2 * KT * DT)
-                    f[n % kAhead] = read(n + kAhead);
+                    o[n % DT] = mfma32<BF>(f[n % kVAhead], pl[n / DT], o[n % DT]);
+                if (n + kVAhead < N)
+                    f[n % kVAhead] = at(n + kVAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if constexpr (PART)
-            if (special)
-                add_special(j0, has, pf);
+        if (special)
+            add_special(j0, has, pf);
     }
 
     // Adds p v for the infinities and NaN of v in block j0, to the rows that see
@@ -319,7 +360,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
             const float p = __shfl(w, 32 * from + col);
             if (!sees(a, p_row, j0 + key))
                 continue;
-            const char *src = vbase + 2 * key_offset(a, a.v_stride, id_of(a, table, j0 + key), j0 + key) + 2 * values + 8 * half;
+            const char *src = vbase + 2 * paging.offset<true>(paging.checked(paging.raw(table, j0 + key)), j0 + key) + 2 * values + 8 * half;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -339,7 +380,7 @@ template <bool BF, int D, bool F32OUT, bool PAGE8> struct ManyRows {
 
 // A share of a row tile's keys.  k and v: two buffers each of a block's rows;
 // they are free again on return.
-template <bool BF, int D, bool F32OUT, bool PAGE8>
+template <bool BF, int D, bool F32OUT, int PAGES>
 __device__ __forceinline__ void run_many(const AttnArgs &a, const Request &rq, int r, int tile, int head, const Share &sh,
                                          char *ka, char *va, char *kb, char *vb)
 {
@@ -347,47 +388,58 @@ __device__ __forceinline__ void run_many(const AttnArgs &a, const Request &rq, i
     constexpr uint64_t kAll = kBlock == 64 ? ~0ull : (1ull << kBlock % 64) - 1; // every key of a block has a page
     __shared__ int lds_last;
     __shared__ uint32_t flags[kWaves];
-    ManyRows<BF, D, F32OUT, PAGE8> t(a);
+    ManyRows<BF, D, F32OUT, PAGES> t(a);
     t.begin(rq, r, tile, head);
     const Walk walk = walk_of<kBlock>(a, t.p_lo, t.p_hi);
     const int b0 = sh.from(walk.count), b1 = sh.to(walk.count);
 
     auto key = [&](int b) { return walk.block(b) * kBlock; };
-    // ids of the block after next, and which keys of this and the next have a page
-    // (an id is checked where it is used, so that its load is waited for there)
-    const auto id_at = [&](int b) { return raw_id(a, t.table, key(b) + t.lane); };
-    int ids = b0 < b1 ? checked_id(a, id_at(b0)) : -1;
-    uint64_t has = 0, has_next = __ballot(ids >= 0);
-    if (b0 < b1)
-        t.fetch(key(b0), ids, ka, va);
-    if (b0 + 1 < b1)
-        ids = id_at(b0 + 1);
+    // Block b's scores are formed during block b - 1, so its k is copied two blocks
+    // ahead and its v one.  id1: checked pages of block b + 1's keys (a lane's key
+    // each), raw2: of block b + 2's as the table has them, so that their load is
+    // waited for where they are used; has0, has1: which keys of b and b + 1 have one.
+    const auto raw_at = [&](int b) { return b < b1 ? t.paging.raw(t.table, key(b) + t.lane) : -1; };
+    int id1 = t.paging.checked(raw_at(b0)), raw2 = raw_at(b0 + 1);
+    uint64_t has0 = __ballot(id1 >= 0), has1 = 0;
+    f32x16 sa[t.KT], sb[t.KT];
+    if (b0 < b1) {
+        t.template fetch<false>(key(b0), id1, ka);
+        t.template fetch<true>(key(b0), id1, va);
+        id1 = t.paging.checked(raw2);
+        has1 = __ballot(id1 >= 0);
+        raw2 = raw_at(b0 + 2);
+        if (b0 + 1 < b1)
+            t.template fetch<false>(key(b0 + 1), id1, kb);
+        __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt(0): this wave's rows are in LDS
+        __syncthreads();
+        t.scores(ka, sa, [](int) {});
+    }
     // The buffers by name in two copies of the step: the compiler then knows that
-    // reads of one need not wait for the copy into the other.
-    const auto step = [&](int b, char *k, char *v, char *knext, char *vnext) {
+    // reads of one need not wait for the copy into the other.  Past the last block
+    // scores are formed of whatever lies in LDS, and dropped.
+    const auto step = [&](int b, char *k, char *knext, char *v, char *vnext, f32x16 *s, f32x16 *next) {
         const int j0 = key(b);
-        has = has_next;
-        __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt(0): this wave's rows of the block are in LDS
-        __syncthreads();                    // everyone's are, and everyone is done with the other buffers
-        if (b + 1 < b1) {
-            ids = checked_id(a, ids);
-            has_next = __ballot(ids >= 0);
-            t.fetch(key(b + 1), ids, knext, vnext);
-            if (b + 2 < b1)
-                ids = id_at(b + 2);
-        }
-        if (!sees_all(a, t.p_lo, t.p_hi, j0, kBlock) || (has & kAll) != kAll) {
-            const bool special = t.clean(j0, has, v, flags);
-            if (t.live && j0 <= t.w_hi)
-                t.template block<true>(j0, has, k, v, special);
-        } else if (t.live) {
-            t.template block<false>(j0, has, k, v, false);
-        }
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+        __syncthreads(); // block b's v and b + 1's k are there; b's k and b - 1's v are done with
+        const int id2 = t.paging.checked(raw2);
+        if (b + 1 < b1)
+            t.template fetch<true>(key(b + 1), id1, vnext);
+        if (b + 2 < b1)
+            t.template fetch<false>(key(b + 2), id2, k);
+        raw2 = raw_at(b + 3);
+        // one body for both kinds of block: in two, the sums would be copied between them
+        const bool part = !sees_all(a, t.p_lo, t.p_hi, j0, kBlock) || (has0 & kAll) != kAll;
+        const bool special = part && t.clean(j0, has0, v, flags);
+        if (t.live)
+            t.block(j0, has0, knext, v, part, special, s, next);
+        has0 = has1;
+        has1 = __ballot(id2 >= 0);
+        id1 = id2;
     };
     for (int b = b0; b < b1; b += 2) {
-        step(b, ka, va, kb, vb);
+        step(b, ka, kb, va, vb, sa, sb);
         if (b + 1 < b1)
-            step(b + 1, kb, vb, ka, va);
+            step(b + 1, kb, ka, vb, va, sb, sa);
     }
 
     if (sh.np > 1) {
