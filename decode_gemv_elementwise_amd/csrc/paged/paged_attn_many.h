@@ -305,6 +305,9 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
         }
         const float base = m == kNegInf ? 0.0f : BF ? m : m - kF16Lift;
         u32x4 pf[2 * KT], pl[F32OUT ? 2 * KT : 1]; // the weights in pairs, and what their rounding lost
+        // the other workgroup's wave on this SIMD starts its copies meanwhile, at the lower
+        // priority: 281 -> 274 us for 2048 new tokens over 8192 keys
+        __builtin_amdgcn_s_setprio(1);
         scores(k, next, [&](int n) {
             constexpr int N = KS * KT, kPairs = 8 * KT;
 #pragma unroll
@@ -338,6 +341,7 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         if (special)
             add_special(j0, has, pf);
     }

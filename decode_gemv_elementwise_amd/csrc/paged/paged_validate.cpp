@@ -5,6 +5,7 @@
 
 #include <climits>
 #include <cmath>
+#include <initializer_list>
 
 namespace gemv {
 namespace {
