@@ -259,7 +259,7 @@ def gemv_paged_attn(q, k_cache, v_cache, block_table, query_start, kv_len, scale
 
 
 def gemv_paged_attn_workspace(dim) -> int:
-    """Bytes of the workspace that never limits gemv_paged_attn's split."""
+    """Bytes of the workspace that is enough for any gemv_paged_attn with heads of ``dim`` values."""
     n = load().gemv_paged_attn_workspace(dim)
     if n < 0:
         binding._raise(int(n))

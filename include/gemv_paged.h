@@ -160,8 +160,8 @@ int gemv_paged_append_validate(const void *q, const void *k, const void *v, int 
  *              are split over workgroups; all zero before its first use and
  *              used by one stream at a time, and left ready for the next call
  *              whatever its shapes.  gemv_paged_attn_workspace gives the size
- *              that never limits the split; with less (0 and NULL included)
- *              the keys are split less.
+ *              that is enough for any call; where it is too small for a call's
+ *              parts (0 and NULL included) no row's keys are split.
  * Sums, the softmax's statistics and the parts are held in 32 bits; the
  * weights w_j are rounded to the cache's type for the product with v (where
  * out is f32 they are carried as two pieces of that type). */
@@ -179,8 +179,8 @@ int gemv_paged_attn_validate(const void *q, int64_t q_token_stride, int64_t q_he
                              int64_t out_token_stride, int64_t out_head_stride, const void *workspace,
                              int64_t workspace_bytes);
 
-/* The workspace that never limits gemv_paged_attn's split for heads of dim
- * values (any lengths), in bytes, or GEMV_E_DIM. */
+/* The workspace that is enough for gemv_paged_attn with heads of dim values
+ * (any lengths), in bytes, or GEMV_E_DIM. */
 int64_t gemv_paged_attn_workspace(int64_t dim);
 
 #ifdef __cplusplus
