@@ -30,11 +30,18 @@ namespace {
 // In blocks of 32 keys: what a workgroup takes at least, and how near a tile's edge
 // a share's end moves to it.  Starting on a tile, and joining its parts, cost about
 // as much as the blocks of `edge`; a block's own time goes by the heads' width.
-constexpr uint32_t least_share(int dim) { return 1024 / dim; }
+// One token over 4099 keys of 128-wide heads: shares of 8 at least 15.6 us, of 16
+// 17.4; with edges of a third (2) 17.6.  A mixed step of 16 requests, 64 wide: edges
+// of 24 38.4 us, of 8 44.8; shares of 32 and edges of 40 40.4.  Drafts of up to 35
+// rows, 256 wide: shares of 8 33.1 us, of 4 37.0, of 12 42.9.
+constexpr uint32_t least_share(int dim) { return dim == 64 ? 16 : 8; }
 constexpr uint32_t few_edge(int dim) { return 1024 / dim; }
 constexpr uint32_t many_edge(int dim) { return 1536 / dim; }
 constexpr uint32_t kMostCost = INT_MAX;
 
+// Up to 16 rows go by the waves' own way: one token over 4099 keys 15.6 us against
+// 26.9 by a tile of many rows, over 131072 keys 105 against 125, 64 single tokens
+// over up to 16384 keys 413 against 425.
 __device__ __forceinline__ bool is_few(const AttnArgs &a, const Request &q) { return (int64_t)q.n * a.group <= kFewRows; }
 
 template <int D> __device__ __forceinline__ uint32_t tiles_of(const AttnArgs &a, const Request &q)
@@ -242,7 +249,10 @@ extern "C" int gemv_paged_attn(const void *q, int64_t q_token_stride, int64_t q_
     a.page = gemv::fast_div(cache->page_size), a.per_group = gemv::fast_div(a.group);
 
     const bool f32out = out_type == GEMV_W_F32;
-    // runs of keys that lie in one page; copies of 16 take 32-bit offsets within a run
+    // Keys from a multiple of 16 (or 8) on that lie in one page are found once for all;
+    // copies of 16 take 32-bit offsets within a run.  2048 new tokens over 8192 keys,
+    // pages of 16: 273 us so, 340 by runs of 8 or key by key; one token over 131072
+    // keys 105 us by runs of 16 or 8, 111 key by key.
     const bool near = a.k_stride[1] < (1u << 27) && a.v_stride[1] < (1u << 27);
     const int pages = cache->page_size % 16 == 0 && near ? 16 : cache->page_size % 8 == 0 ? 8 : 0;
     const void *fn = cache->dim == 64    ? gemv::kernel_of<64>(cache->type, f32out, pages)
@@ -257,7 +267,7 @@ extern "C" int gemv_paged_attn(const void *q, int64_t q_token_stride, int64_t q_
            (blocks + (1ll << a.unit_log2) - 1) >> a.unit_log2 > (INT_MAX - 1) / tiles)
         ++a.unit_log2;
     const int64_t most = gemv::kAttnGroups;
-    const int64_t shares = (blocks + gemv::least_share(256) - 1) / gemv::least_share(256);
+    const int64_t shares = (blocks + gemv::least_share(128) - 1) / gemv::least_share(128);
     const int grid = (int)(tiles >= most || shares >= most || tiles * shares >= most ? most : tiles * shares);
     void *args[] = {&a};
     const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)grid), dim3(gemv::kThreads), args, 0,

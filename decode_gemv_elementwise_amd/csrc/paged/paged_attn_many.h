@@ -20,6 +20,11 @@
 // permuted by the row, so that the products' reads meet no bank twice (k_turn,
 // v_turn).
 //
+// Bound by the matrix cores and the exponentials beside them: 2048 new tokens over
+// 8192 keys (240 GFLOP, 32 query and 8 key/value heads of 128) take 255 to 273 us,
+// 880 to 944 TFLOP/s.  Of a block's 3600 cycles a wave (two share a SIMD) 2550 are
+// products and weights, 900 the start of the next copies and 140 waits.
+//
 // The running maximum only moves when a row's new one is more than kSlack above
 // it (weights up to 2^kSlack are as good as weights up to 1): most blocks then
 // skip the pass over the 32 x D sums.

@@ -5,6 +5,7 @@ import random
 import pytest
 import torch
 
+import paged_ref
 from decode_gemv_elementwise_amd import binding, paged
 from test_gpu_paged import Case, I32, ints, run_append
 
@@ -150,6 +151,22 @@ def test_more_tokens_than_a_grid_has_rows():
     """Rotary append past 2^16 tokens, wide rows and odd ones."""
     run_append("bf16", "bf16", 70001, 1, 1, 16, 16, 1, "halves", 64)
     run_append("f16", "f16", 65537, 1, 1, 8, 6, 1, "pairs", 64)
+
+
+def test_far_pages_of_a_chunk():
+    """A cache of more than 2^31 elements, its last pages used by a tile of many rows."""
+    pages = 2 ** 31 // (16 * 8 * 128) + 40
+    c = Case([(20, 300), (1, 60)], "bf16", 16, 8, 128)
+    k, v = (torch.empty((pages, 16, 8, 128), device="cuda", dtype=torch.bfloat16) for _ in "kv")
+    small = c.k.shape[0]
+    k[-small:], v[-small:] = c.k, c.v
+    y, bound, _ = paged_ref.attn(c.q, c.k, c.v, ints(c.table, "cpu"), ints(c.starts, "cpu"), ints(c.lens, "cpu"), c.scale,
+                                 0, 0, torch.bfloat16)
+    table = ints(c.table)
+    table = torch.where(table >= 0, table + (pages - small), table)
+    out = torch.empty_like(c.q)
+    paged.gemv_paged_attn(c.q, k, v, table, ints(c.starts), ints(c.lens), c.scale, out, c.work)
+    assert ((out.double().cpu() - y).abs() <= bound).all()
 
 
 # ------------------------------------------------------------------ the binding
