@@ -2,7 +2,8 @@
 //
 // Memory-bound: every value of q, k and v is read once and written once, so
 // the kernel is one pass with 16-byte accesses: 8192 tokens of 32 + 2 x 8 heads of
-// 128 in 40.6 us, 4.96 TB/s read and written, where a large copy reaches 4.87.  A workgroup takes one token
+// 128 in 40.6 us, 4.96 TB/s read and written, where a large copy reaches 4.87 (42.6
+// with a loop over tokens around it).  A workgroup takes one token
 // (or, for few tokens, a share of one token's heads): its first threads form
 // the cosines and sines of that token's rot / 2 angles, once for all heads,
 // while the workgroup's first rows are on their way from memory.
@@ -17,7 +18,7 @@
 namespace gemv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kTokensX = 65536;
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -134,6 +135,10 @@ __device__ __forceinline__ void item_of(const AppendArgs &a, int item, int *whic
     }
 }
 
+// A workgroup's token: a grid's x counts its threads in 32 bits, so past 2^16
+// tokens z goes on.
+__device__ __forceinline__ int token_here() { return blockIdx.z * kTokensX + blockIdx.x; }
+
 // The wide path.  An item is 8 neighbouring values, or for halves 8 values of
 // the first half together with their 8 partners: rot is a multiple of 16 for
 // halves (8 for pairs), so no vector straddles the halves or the end of rot.
@@ -141,59 +146,57 @@ template <class S, class D, bool PAIRS>
 __global__ __launch_bounds__(kThreads) void paged_append_kernel(AppendArgs a)
 {
     extern __shared__ float2 turns[];
-    for (int t = blockIdx.x;; t += gridDim.x) {
-        const int slot = a.slots[t];
-        bool filled = false;
-        for (int item = blockIdx.y * kThreads + threadIdx.x;; item += gridDim.y * kThreads) {
-            // the first rows are asked for before the angles are formed
-            int which = 0, head = 0, at = 0, lo = 0, hi = 0;
-            float u[8], w[8];
-            const bool live = item < a.total;
-            bool turn = false, two = false;
-            if (live) {
-                item_of(a, item, &which, &head, &at);
-                if (PAIRS) {
-                    lo = 8 * at;
-                    turn = which < 2 && lo < 2 * a.half;
-                } else {
-                    two = which < 2 && 8 * at < a.half;
-                    turn = two;
-                    lo = which < 2 && !two ? a.half + 8 * at : 8 * at;
-                    hi = lo + a.half;
-                }
-                const S *row = static_cast<const S *>(a.src[which]) + (int64_t)t * a.src_stride[which] + head * a.dim;
-                load8(row + lo, u);
-                if (two)
-                    load8(row + hi, w);
+    const int t = token_here();
+    if (t >= a.tokens)
+        return;
+    const int slot = a.slots[t];
+    bool filled = false;
+    for (int item = blockIdx.y * kThreads + threadIdx.x;; item += gridDim.y * kThreads) {
+        // the first rows are asked for before the angles are formed
+        int which = 0, head = 0, at = 0, lo = 0, hi = 0;
+        float u[8], w[8];
+        const bool live = item < a.total;
+        bool turn = false, two = false;
+        if (live) {
+            item_of(a, item, &which, &head, &at);
+            if (PAIRS) {
+                lo = 8 * at;
+                turn = which < 2 && lo < 2 * a.half;
+            } else {
+                two = which < 2 && 8 * at < a.half;
+                turn = two;
+                lo = which < 2 && !two ? a.half + 8 * at : 8 * at;
+                hi = lo + a.half;
             }
-            if (!filled) {
-                fill_turns(a, t, turns);
-                __syncthreads();
-                filled = true;
-            }
-            if (live) {
-                if (turn) {
-#pragma unroll
-                    for (int i = 0; i < (PAIRS ? 4 : 8); ++i) {
-                        float &x = PAIRS ? u[2 * i] : u[i], &y = PAIRS ? u[2 * i + 1] : w[i];
-                        const float2 cs = turns[PAIRS ? lo / 2 + i : lo + i];
-                        const float nx = fmaf(x, cs.x, -(y * cs.y)), ny = fmaf(y, cs.x, x * cs.y);
-                        x = nx;
-                        y = ny;
-                    }
-                }
-                if (D *out = row_out<D>(a, t, which, head, slot)) {
-                    store8(out + lo, u);
-                    if (two)
-                        store8(out + hi, w);
-                }
-            }
-            if (item - (int)threadIdx.x + (int)(gridDim.y * kThreads) >= a.total)
-                break;
+            const S *row = static_cast<const S *>(a.src[which]) + (int64_t)t * a.src_stride[which] + head * a.dim;
+            load8(row + lo, u);
+            if (two)
+                load8(row + hi, w);
         }
-        if (a.tokens - t <= (int)gridDim.x)
+        if (!filled) {
+            fill_turns(a, t, turns);
+            __syncthreads();
+            filled = true;
+        }
+        if (live) {
+            if (turn) {
+#pragma unroll
+                for (int i = 0; i < (PAIRS ? 4 : 8); ++i) {
+                    float &x = PAIRS ? u[2 * i] : u[i], &y = PAIRS ? u[2 * i + 1] : w[i];
+                    const float2 cs = turns[PAIRS ? lo / 2 + i : lo + i];
+                    const float nx = fmaf(x, cs.x, -(y * cs.y)), ny = fmaf(y, cs.x, x * cs.y);
+                    x = nx;
+                    y = ny;
+                }
+            }
+            if (D *out = row_out<D>(a, t, which, head, slot)) {
+                store8(out + lo, u);
+                if (two)
+                    store8(out + hi, w);
+            }
+        }
+        if (item - (int)threadIdx.x + (int)(gridDim.y * kThreads) >= a.total)
             break;
-        __syncthreads(); // the turns are read; the next token's may be written
     }
 }
 
@@ -202,31 +205,29 @@ template <class S, class D>
 __global__ __launch_bounds__(kThreads) void paged_append_generic_kernel(AppendArgs a)
 {
     extern __shared__ float2 turns[];
-    for (int t = blockIdx.x;; t += gridDim.x) {
-        const int slot = a.slots[t];
-        fill_turns(a, t, turns);
-        __syncthreads();
-        for (int item = blockIdx.y * kThreads + threadIdx.x; item < a.total; item += gridDim.y * kThreads) {
-            int which, head, at;
-            item_of(a, item, &which, &head, &at);
-            const S *row = static_cast<const S *>(a.src[which]) + (int64_t)t * a.src_stride[which] + head * a.dim;
-            D *out = row_out<D>(a, t, which, head, slot);
-            if (!out)
-                continue;
-            if (which < 2 && at < a.half) {
-                const int lo = a.pairs ? 2 * at : at, hi = a.pairs ? lo + 1 : lo + a.half;
-                const float x = (float)row[lo], y = (float)row[hi];
-                const float2 cs = turns[at];
-                out[lo] = (D)fmaf(x, cs.x, -(y * cs.y));
-                out[hi] = (D)fmaf(y, cs.x, x * cs.y);
-            } else {
-                const int e = which < 2 ? a.half + at : at;
-                out[e] = (D)(float)row[e];
-            }
+    const int t = token_here();
+    if (t >= a.tokens)
+        return;
+    const int slot = a.slots[t];
+    fill_turns(a, t, turns);
+    __syncthreads();
+    for (int item = blockIdx.y * kThreads + threadIdx.x; item < a.total; item += gridDim.y * kThreads) {
+        int which, head, at;
+        item_of(a, item, &which, &head, &at);
+        const S *row = static_cast<const S *>(a.src[which]) + (int64_t)t * a.src_stride[which] + head * a.dim;
+        D *out = row_out<D>(a, t, which, head, slot);
+        if (!out)
+            continue;
+        if (which < 2 && at < a.half) {
+            const int lo = a.pairs ? 2 * at : at, hi = a.pairs ? lo + 1 : lo + a.half;
+            const float x = (float)row[lo], y = (float)row[hi];
+            const float2 cs = turns[at];
+            out[lo] = (D)fmaf(x, cs.x, -(y * cs.y));
+            out[hi] = (D)fmaf(y, cs.x, x * cs.y);
+        } else {
+            const int e = which < 2 ? a.half + at : at;
+            out[e] = (D)(float)row[e];
         }
-        if (a.tokens - t <= (int)gridDim.x)
-            break;
-        __syncthreads(); // the turns are read; the next token's may be written
     }
 }
 
@@ -291,9 +292,9 @@ extern "C" int gemv_paged_append(const void *q, const void *k, const void *v, in
                      : src_type == GEMV_W_F16 ? gemv::kernel_of<_Float16>(cache->type, wide, a.pairs)
                                               : gemv::kernel_of<__bf16>(cache->type, wide, a.pairs);
     void *args[] = {&a};
-    // a workgroup takes every 2^16-th token: a grid's threads are counted in 32 bits
-    const unsigned groups = (unsigned)(tokens < 65536 ? tokens : 65536);
-    const hipError_t e = hipLaunchKernel(fn, dim3(groups, (unsigned)parts), dim3(gemv::kThreads), args,
-                                         (size_t)a.half * sizeof(float2), static_cast<hipStream_t>(hip_stream));
+    const int64_t x = tokens < gemv::kTokensX ? tokens : gemv::kTokensX;
+    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)x, (unsigned)parts, (unsigned)((tokens + x - 1) / x)),
+                                         dim3(gemv::kThreads), args, (size_t)a.half * sizeof(float2),
+                                         static_cast<hipStream_t>(hip_stream));
     return gemv::finish_launch((int)e);
 }
