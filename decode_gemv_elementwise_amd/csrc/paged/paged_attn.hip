@@ -52,8 +52,9 @@ template <int D> __device__ __forceinline__ uint32_t tiles_of(const AttnArgs &a,
 
 // What the plan counts for a row tile of the request: its blocks of 32 keys, the
 // most that one tile visits (in units of 2^unit_log2 blocks, which is 1 unless
-// the line would be longer than 2^31), and at least one, so that every row is
-// written.
+// the line would be longer than 2^31), and tile_cost for starting on it: many
+// short tiles then spread over the card (21 requests of 16 keys and 8 heads each
+// took 62 us where ten workgroups shared them).
 template <int D> __device__ __forceinline__ uint32_t cost_of(const AttnArgs &a, const Request &q)
 {
     uint32_t keys = (uint32_t)min((int64_t)q.kv, a.reach);
@@ -61,7 +62,7 @@ template <int D> __device__ __forceinline__ uint32_t cost_of(const AttnArgs &a, 
         const uint32_t some = (uint32_t)a.window + min(q.n, many_rows(D)) + 4 * kFewBlock; // below 2^32
         keys = min(keys, min((uint32_t)a.sinks, keys) + min(some, keys));
     }
-    return max((keys + kFewBlock - 1) / kFewBlock >> a.unit_log2, 1u);
+    return ((keys + kFewBlock - 1) / kFewBlock >> a.unit_log2) + a.tile_cost;
 }
 
 // The kernel's arguments, read again from here on: the two kinds of tile need
@@ -263,11 +264,13 @@ extern "C" int gemv_paged_attn(const void *q, int64_t q_token_stride, int64_t q_
     const int64_t blocks = (a.reach + gemv::kFewBlock - 1) / gemv::kFewBlock;
     int64_t tiles = tokens * a.group / gemv::kFewRows + (requests < tokens ? requests : tokens);
     tiles = (tiles < tokens * a.group ? tiles : tokens * a.group) * a.heads; // at most tokens * q_heads, below 2^31
-    while ((blocks + (1ll << a.unit_log2) - 1) >> a.unit_log2 > 1 &&
-           (blocks + (1ll << a.unit_log2) - 1) >> a.unit_log2 > (INT_MAX - 1) / tiles)
+    const int64_t cap = (INT_MAX - 1) / tiles; // of a tile's cost
+    const int64_t start = gemv::least_share(cache->dim);
+    a.tile_cost = (int)(start <= cap / 2 ? start : cap > 1 ? cap / 2 : 1);
+    while (a.tile_cost + (blocks >> a.unit_log2) > cap)
         ++a.unit_log2;
     const int64_t most = gemv::kAttnGroups;
-    const int64_t shares = (blocks + gemv::least_share(128) - 1) / gemv::least_share(128);
+    const int64_t shares = (blocks + a.tile_cost) / gemv::least_share(128) + 1;
     const int grid = (int)(tiles >= most || shares >= most || tiles * shares >= most ? most : tiles * shares);
     void *args[] = {&a};
     const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)grid), dim3(gemv::kThreads), args, 0,

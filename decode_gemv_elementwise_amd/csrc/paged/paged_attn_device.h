@@ -30,7 +30,7 @@ struct AttnArgs {
     int32_t *counters;
     float *parts;
     int64_t part_room;           // floats that the workspace has for parts
-    int32_t width, requests, tokens, heads, group, num_pages, window, sinks, unit_log2;
+    int32_t width, requests, tokens, heads, group, num_pages, window, sinks, unit_log2, tile_cost;
     int64_t reach;               // keys that a table row can hold
     float scale_log2;            // |scale| log2(e); its sign is in q_flip
     uint32_t q_keep, q_flip;     // q's words are (x & q_keep) ^ q_flip: scale 0 takes q as 0
