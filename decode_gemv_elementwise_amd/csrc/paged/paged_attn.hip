@@ -29,14 +29,14 @@ namespace {
 
 // In blocks of 32 keys: what a workgroup takes at least, and how near a tile's edge
 // a share's end moves to it.  Starting on a tile, and joining its parts, cost about
-// as much as the blocks of `edge`; a block's own time goes by the heads' width.
-// One token over 4099 keys of 128-wide heads: shares of 8 at least 15.6 us, of 16
-// 17.4; with edges of a third (2) 17.6.  A mixed step of 16 requests, 64 wide: edges
-// of 24 38.4 us, of 8 44.8; shares of 32 and edges of 40 40.4.  Drafts of up to 35
-// rows, 256 wide: shares of 8 33.1 us, of 4 37.0, of 12 42.9.
+// as much as the blocks of `edge`.  One token over 4099 keys of 128-wide heads:
+// shares of 8 at least 15.6 us, of 16 17.4; with edges of 2 17.6.  A mixed step of
+// 16 requests, 64 wide: edges of 24 37.5 us, of 8 44.8; shares of 32 and edges of 40
+// 40.4.  Drafts of up to 35 rows, 256 wide: shares of 8 33.5 us, of 4 37.0, of 12
+// 42.9; requests of 3 keys there 12 us, with edges of 4, which cut their tiles, 24.
 constexpr uint32_t least_share(int dim) { return dim == 64 ? 16 : 8; }
-constexpr uint32_t few_edge(int dim) { return 1024 / dim; }
-constexpr uint32_t many_edge(int dim) { return 1536 / dim; }
+constexpr uint32_t few_edge(int dim) { return least_share(dim); }
+constexpr uint32_t many_edge(int dim) { return dim == 64 ? 24 : dim == 128 ? 12 : 8; }
 constexpr uint32_t kMostCost = INT_MAX;
 
 // Up to 16 rows go by the waves' own way: one token over 4099 keys 15.6 us against
