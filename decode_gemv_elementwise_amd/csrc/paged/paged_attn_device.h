@@ -13,7 +13,9 @@ constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr float kNegInf = -__builtin_inff();
 // A weight 2^(s - m) of binary16 is carried 2^14 times its size (the sums l and
 // over v alike, so it cancels): its smallest step, 2^-24, would otherwise lose
-// the many small weights of a long row beside one large one.
+// the many small weights of a long row beside one large one.  It is added to s - m:
+// folded into m it is lost, or grows to 16 and past binary16, where m is so large
+// that a step of 32 bits is 2 or more.
 constexpr float kF16Lift = 14.0f;
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));

@@ -193,10 +193,10 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct FewRows {
                 o[i] *= f;
             m = top;
         }
-        const float base = m == kNegInf ? 0.0f : BF ? m : m - kF16Lift;
+        const float base = m == kNegInf ? 0.0f : m;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            p[i] = __builtin_amdgcn_exp2f(p[i] - base);
+            p[i] = __builtin_amdgcn_exp2f(BF ? p[i] - base : p[i] - base + kF16Lift);
             l += p[i];
         }
         bool special = false;

@@ -75,6 +75,8 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
     static constexpr int kAhead = 2, kVAhead = 2; // products between a read of LDS and its use
     // binary16's weights are lifted, which leaves one power of two to its largest
     static constexpr float kSlack = BF ? 8.0f : 1.0f;
+    // m of this size has steps of 2^-16 (and 2^-17 below): what its rounding moves a weight by
+    static constexpr float kFar = 128.0f;
 
     const AttnArgs &a;
     const char *kbase, *vbase; // of the key/value head
@@ -299,7 +301,7 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
             for (int i = 0; i < 16; ++i)
                 top = fmaxf(top, s[t][i]);
         top = half_max(top) * scale;
-        if (__any(top > m + kSlack)) {
+        if (__any(top - m > kSlack)) { // by the difference: m + kSlack may round up a step
             const float to = fmaxf(m, top);
             const float f = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
             l *= f;
@@ -308,7 +310,24 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
                 o[d] *= f;
             m = to;
         }
-        const float base = m == kNegInf ? 0.0f : BF ? m : m - kF16Lift;
+        // A weight is 2^(by s - off): one fused step, whose s scale is exact where m is
+        // s scale rounded.  From kFar on that difference shows, and from 2^24 it can
+        // take a weight past binary16 or down to 0: there the scores are replaced by
+        // s scale - m, both rounded alike, first (2048 new tokens over 8192 keys: 263 us
+        // against 247).  With keys found one by one always: the branch would cost tiles
+        // of few rows their registers (64 single tokens over up to 8192 keys, pages of
+        // 5: 240 us against 226; 2048 over 8192 332 against 336).
+        const float base = m == kNegInf ? 0.0f : m;
+        float by = scale, off = BF ? base : base - kF16Lift;
+        if (PAGES == 0 || __any(__builtin_fabsf(base) >= kFar)) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[t][i] = s[t][i] * scale - base;
+            by = 1.0f;
+            off = BF ? 0.0f : -kF16Lift;
+        }
         u32x4 pf[2 * KT], pl[F32OUT ? 2 * KT : 1]; // the weights in pairs, and what their rounding lost
         // the other workgroup's wave on this SIMD starts its copies meanwhile, at the lower
         // priority: 281 -> 274 us for 2048 new tokens over 8192 keys
@@ -320,7 +339,7 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
                 float p[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    p[i] = __builtin_amdgcn_exp2f(fmaf(s[e / 8][2 * e % 16 + i], scale, -base));
+                    p[i] = __builtin_amdgcn_exp2f(fmaf(s[e / 8][2 * e % 16 + i], by, -off));
                     l += p[i];
                 }
                 pf[e / 4][e % 4] = round2<BF>(p);
