@@ -86,32 +86,53 @@ template <bool BF> __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f3
                                                       0, 0);
 }
 
-// Eight floats rounded to nearest into 16 bits, and what each lost.
-template <bool BF> __device__ __forceinline__ u32x4 round8(const float *p, float *rest)
+// Eight floats rounded to nearest into 16 bits.
+template <bool BF> __device__ __forceinline__ u32x4 round8(const float *p)
 {
     typedef typename std::conditional<BF, bf16x8, f16x8>::type T8;
     typedef typename std::conditional<BF, __bf16, _Float16>::type T;
     T8 r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i)
         r[i] = (T)p[i];
-        rest[i] = p[i] - (float)r[i];
-    }
     return __builtin_bit_cast(u32x4, r);
 }
 
-// Two floats rounded to nearest into 16 bits; p gets what each lost.
-template <bool BF> __device__ __forceinline__ uint32_t round2(float *p)
+// Two floats rounded to nearest into 16 bits.
+template <bool BF> __device__ __forceinline__ uint32_t round2(const float *p)
 {
     typedef typename std::conditional<BF, __bf16, _Float16>::type T;
     typedef T t2 __attribute__((ext_vector_type(2)));
     t2 r;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i)
         r[i] = (T)p[i];
-        p[i] -= (float)r[i];
-    }
     return __builtin_bit_cast(uint32_t, r);
+}
+
+// Two floats from 0 up as two pieces of 16 bits each, for a result of 32: the first
+// piece is returned, p gets the rest.  The first lies below p, so that the rest is
+// above 0 and an infinity of v times either is that infinity; a piece of 0, which
+// rounding to nearest leaves of a weight of 1, would make it NaN.  Together they are
+// within 2^-16 (bf16) and 2^-21 (binary16) of p.
+template <bool BF> __device__ __forceinline__ uint32_t split2(float *p)
+{
+    if constexpr (BF) {
+        const uint32_t a = __builtin_elementwise_sub_sat(__builtin_bit_cast(uint32_t, p[0]), 1u);
+        const uint32_t b = __builtin_elementwise_sub_sat(__builtin_bit_cast(uint32_t, p[1]), 1u);
+        p[0] -= __builtin_bit_cast(float, a & 0xffff0000u);
+        p[1] -= __builtin_bit_cast(float, b & 0xffff0000u);
+        return __builtin_amdgcn_perm(b, a, 0x07060302u);
+    } else {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+        const u16x2 r = __builtin_elementwise_sub_sat(
+            __builtin_bit_cast(u16x2, __builtin_amdgcn_cvt_pkrtz(p[0], p[1])), u16x2{1, 1});
+        const f16x2 f = __builtin_bit_cast(f16x2, r);
+        p[0] -= (float)f[0];
+        p[1] -= (float)f[1];
+        return __builtin_bit_cast(uint32_t, r);
+    }
 }
 
 template <bool BF> __device__ __forceinline__ float as_float(uint16_t x)

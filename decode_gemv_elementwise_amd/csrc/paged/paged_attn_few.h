@@ -226,12 +226,18 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct FewRows {
                     }
             }
         }
-        float rest[8];
-        const u32x4 pf = round8<BF>(p, rest);
-        u32x4 pl;
+        u32x4 pf, pl; // the weights in 16 bits; the second piece of them
         if constexpr (F32OUT) {
-            float none[8];
-            pl = round8<BF>(rest, none);
+            float rest[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                rest[i] = p[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pf[i] = split2<BF>(rest + 2 * i);
+            pl = round8<BF>(rest);
+        } else {
+            pf = round8<BF>(p);
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {

@@ -328,7 +328,7 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
             by = 1.0f;
             off = BF ? 0.0f : -kF16Lift;
         }
-        u32x4 pf[2 * KT], pl[F32OUT ? 2 * KT : 1]; // the weights in pairs, and what their rounding lost
+        u32x4 pf[2 * KT], pl[F32OUT ? 2 * KT : 1]; // the weights in pairs, and the second piece of them
         // the other workgroup's wave on this SIMD starts its copies meanwhile, at the lower
         // priority: 281 -> 274 us for 2048 new tokens over 8192 keys
         __builtin_amdgcn_s_setprio(1);
@@ -342,9 +342,12 @@ template <bool BF, int D, bool F32OUT, int PAGES> struct ManyRows {
                     p[i] = __builtin_amdgcn_exp2f(fmaf(s[e / 8][2 * e % 16 + i], by, -off));
                     l += p[i];
                 }
-                pf[e / 4][e % 4] = round2<BF>(p);
-                if constexpr (F32OUT)
+                if constexpr (F32OUT) {
+                    pf[e / 4][e % 4] = split2<BF>(p);
                     pl[e / 4][e % 4] = round2<BF>(p);
+                } else {
+                    pf[e / 4][e % 4] = round2<BF>(p);
+                }
             }
         });
         {

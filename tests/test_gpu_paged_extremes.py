@@ -1,4 +1,5 @@
-"""The paged attention at scores far beyond a trained head's, in rows few and many."""
+"""The paged attention at scores far beyond a trained head's, and at infinities
+and NaN of v beside a result in 32 bits, in rows few and many."""
 import math
 
 import pytest
@@ -102,3 +103,16 @@ def test_steps_of_the_score_above_the_slack():
             w = torch.tensor([2.0 ** (step[j] - step[p]) for j in range(p + 1)], dtype=torch.float64)
             want[row] = (w[:, None, None] * v[:p + 1]).sum(0) / w.sum()
         held(c, want, torch.float16)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_special_values_in_float32_results(value, dtype, dim):
+    """An infinity or NaN of v in keys that all rows see, that some see, and behind the window."""
+    for window in (0, 300):
+        c = Case([(40, 1200), (3, 500), (1, 2000), (1, 1)], dtype, 2, 1, dim, seed=5)
+        c.window, c.sinks = window, 3
+        for r, j in ((0, 20), (0, 1175), (1, 470), (1, 1), (2, 40), (2, 1990), (3, 0)):
+            key(c, c.v, r, j)[0, 7 + j % 3] = value
+        c.check(c.run(torch.float32), f"{value} window {window}")
