@@ -164,7 +164,9 @@ int gemv_paged_append_validate(const void *q, const void *k, const void *v, int 
  *              parts (0 and NULL included) no row's keys are split.
  * Sums, the softmax's statistics and the parts are held in 32 bits; the
  * weights w_j are rounded to the cache's type for the product with v (where
- * out is f32 they are carried as two pieces of that type). */
+ * out is f32 they are carried as two pieces of that type).  An infinity of v
+ * whose weight is too small to be held beside the row's largest (binary16: below
+ * 2^-38 of it) gives that infinity or NaN, by where in the row its key lies. */
 int gemv_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, const gemv_kv_cache *cache,
                     const int32_t *block_table, int64_t table_width, int64_t table_stride, const int32_t *query_start,
                     const int32_t *kv_len, int64_t requests, int64_t tokens, int64_t q_heads, float scale,

@@ -116,3 +116,22 @@ def test_special_values_in_float32_results(value, dtype, dim):
         for r, j in ((0, 20), (0, 1175), (1, 470), (1, 1), (2, 40), (2, 1990), (3, 0)):
             key(c, c.v, r, j)[0, 7 + j % 3] = value
         c.check(c.run(torch.float32), f"{value} window {window}")
+
+
+def test_infinities_beside_weights_that_binary16_does_not_hold():
+    """An infinity whose weight is 2^-57 of the largest: itself or NaN in every row that sees its key, by where in the
+    row that lies, and nothing of it in the other rows."""
+    for lens, at in (([(1, 40), (1, 40)], (3, 39)), ([(20, 100), (20, 100)], (3, 85))):
+        c = Case(lens, "f16", 2, 1, 64, seed=6)
+        c.q[:], c.k[:] = 0, 0
+        c.q[..., 0] = 8
+        for r in range(2):
+            key(c, c.k, r, 10)[..., 0] = 40  # a score of 40, the others' is 0
+            key(c, c.v, r, at[r])[..., 9] = float("inf")
+        want = torch.zeros(c.q.shape, dtype=torch.bool)
+        for row, r, p in rows_of(c):
+            want[row, :, 9] = p >= at[r]
+        for out in (torch.float16, torch.float32):
+            got = c.run(out).cpu()
+            assert torch.isfinite(got).equal(~want), f"{lens} {out}"
+            assert not (got == float("-inf")).any()
