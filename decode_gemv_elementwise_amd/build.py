@@ -7,7 +7,10 @@ hipcc cross-compiles without a GPU.  Flags:
   -packed-fp32-ops off  no packed FP32 instructions are generated.
 """
 import os
+import shutil
 import subprocess
+import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -66,10 +69,21 @@ def build_cpu(verbose: bool = False) -> str:
     return CPU_LIB
 
 
+def python_module_needs() -> str:
+    """What the Python module cannot be built for want of on this host; empty if nothing."""
+    if shutil.which("g++") is None:
+        return "g++ is not installed"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers are not installed"
+    try:
+        import torch  # noqa: F401
+    except ImportError as e:
+        return f"torch cannot be imported ({e})"
+    return ""
+
+
 def build_python(verbose: bool = False) -> str:
     """The CPython module that marshals the paged operators' tensors (host code)."""
-    import sysconfig
-
     import torch
 
     root = os.path.dirname(torch.__file__)
@@ -86,12 +100,19 @@ def build_python(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Builds the GEMV library, the benchmark's measurement library, the CPU
-    comparison GEMV and the paged operators' Python module."""
+    """Builds the benchmark's measurement library, the CPU comparison GEMV and
+    the GEMV library, which need hipcc and gcc alone, and last the paged
+    operators' Python module, which is left out where the host has no torch,
+    g++ or Python headers: ``paged`` then checks its tensors in Python."""
     _compile(PROBE_SOURCES, PROBE_LIB, verbose)
     build_cpu(verbose)
-    build_python(verbose)
-    return _compile(SOURCES, LIB, verbose)
+    lib = _compile(SOURCES, LIB, verbose)
+    missing = python_module_needs()
+    if missing:
+        print(f"{os.path.basename(PY_LIB)} is not built: {missing}", file=sys.stderr)
+    else:
+        build_python(verbose)
+    return lib
 
 
 if __name__ == "__main__":

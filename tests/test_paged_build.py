@@ -1,0 +1,43 @@
+"""The library is built, and the paged operators work, without the Python module
+that marshals their tensors."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from decode_gemv_elementwise_amd import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture
+def steps(monkeypatch):
+    """build() with its compilations recorded in place of run."""
+    done = []
+    monkeypatch.setattr(build, "_compile", lambda sources, out, verbose: done.append(out) or out)
+    monkeypatch.setattr(build, "build_cpu", lambda verbose=False: done.append(build.CPU_LIB))
+    monkeypatch.setattr(build, "_run", lambda cmd, verbose: done.append(cmd))
+    monkeypatch.setattr(build.os, "replace", lambda a, b: done.append(b))
+    return done
+
+
+def test_library_is_built_before_the_module(steps):
+    pytest.importorskip("torch")
+    assert build.build() == build.LIB
+    assert steps.index(build.LIB) < steps.index(build.PY_LIB) == len(steps) - 1
+
+
+def test_library_is_built_without_torch(steps, monkeypatch, capsys):
+    monkeypatch.setitem(sys.modules, "torch", None)
+    assert build.build() == build.LIB
+    assert build.LIB in steps and build.CPU_LIB in steps and build.PY_LIB not in steps
+    assert "torch" in capsys.readouterr().err
+
+
+def test_library_is_built_without_a_cpp_compiler(steps, monkeypatch, capsys):
+    pytest.importorskip("torch")
+    monkeypatch.setattr(build.shutil, "which", lambda name: None)
+    assert build.build() == build.LIB
+    assert build.LIB in steps and build.PY_LIB not in steps
+    assert "g++" in capsys.readouterr().err
