@@ -11,7 +11,8 @@ made on has to be kept alive, or recorded on that stream, by the caller.
 
 Calls go through ``_paged_fast`` first (C++, 1 us a call where the same checks
 here take 6); what it does not take at once comes to the checks below, which
-accept the call or raise.
+accept the call or raise.  Where that module is not built, or is another
+interpreter's, every call goes through the checks here.
 
 A cache is a pair of tensors ``[pages, page_size, heads, dim]`` of float16 or
 bfloat16 with any strides whose innermost is 1 (a ``[pages, heads, page_size,
@@ -34,8 +35,8 @@ class GemvKvCache(ctypes.Structure):
 
 _CACHEP = ctypes.POINTER(GemvKvCache)
 _LIB = None
-_FAST = None      # the module that checks and marshals a call's tensors at once
-_DEVICE = None    # () -> index of the current GPU, -1 if there is none
+_FAST = None      # the module that checks and marshals a call's tensors at once, if it is built
+_DEVICE = None    # () -> index of the current GPU, -1 if there is none or no module
 
 
 def load():
@@ -59,13 +60,14 @@ def load():
     TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
     try:
         from . import _paged_fast
-    except ImportError as e:
-        raise ImportError(f"{e}; build it with: python -m decode_gemv_elementwise_amd.build") from e
-    _paged_fast.bind(*(ctypes.cast(getattr(lib, f), _VP).value
-                       for f in ("gemv_paged_slots", "gemv_paged_append", "gemv_paged_attn")))
-    _FAST = _paged_fast
-    raw = getattr(torch._C, "_cuda_getDevice", None)
-    _DEVICE = (raw or torch.cuda.current_device) if torch.cuda.is_available() else lambda: -1
+    except ImportError:
+        _paged_fast = None
+    _FAST, _DEVICE = _paged_fast, lambda: -1
+    if _FAST is not None:
+        _FAST.bind(*(ctypes.cast(getattr(lib, f), _VP).value
+                     for f in ("gemv_paged_slots", "gemv_paged_append", "gemv_paged_attn")))
+        if torch.cuda.is_available():
+            _DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _LIB = lib
     return lib
 

@@ -41,3 +41,27 @@ def test_library_is_built_without_a_cpp_compiler(steps, monkeypatch, capsys):
     assert build.build() == build.LIB
     assert build.LIB in steps and build.PY_LIB not in steps
     assert "g++" in capsys.readouterr().err
+
+
+def test_paged_loads_without_the_module():
+    """The checks and the refusals in Python serve where the module is missing."""
+    pytest.importorskip("torch")
+    if not os.path.exists(build.LIB):  # pragma: no cover - the build step makes it
+        pytest.skip("the library is not built")
+    code = """
+import sys
+sys.modules["decode_gemv_elementwise_amd._paged_fast"] = None
+import torch
+from decode_gemv_elementwise_amd import paged
+assert paged.load() is not None and paged._FAST is None
+assert paged.gemv_paged_attn_workspace(64) > 0
+ints = lambda n: torch.zeros(n, dtype=torch.int32)
+try:
+    paged.gemv_paged_slots(ints(2), ints(2), ints(4), 16, ints(8).view(2, 4), ints(3), ints(2), ints(3), ints(3), ints(3), ints(1))
+except TypeError as e:
+    assert "GPU" in str(e)
+    print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.strip() == "refused"
