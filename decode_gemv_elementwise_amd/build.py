@@ -20,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgemv_fused.so")
 PY_SOURCE = os.path.join(CSRC, "paged", "paged_python.cpp")
-PY_LIB = os.path.join(HERE, "_paged_fast.so")
+# named for the interpreter that it is built for: another one does not load it
+PY_LIB = os.path.join(HERE, "_paged_fast" + sysconfig.get_config_var("EXT_SUFFIX"))
 PROBE_LIB = os.path.join(HERE, "libhbm_probe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

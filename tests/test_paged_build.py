@@ -43,6 +43,15 @@ def test_library_is_built_without_a_cpp_compiler(steps, monkeypatch, capsys):
     assert "g++" in capsys.readouterr().err
 
 
+def test_module_is_named_for_its_interpreter():
+    import importlib.machinery
+    import sysconfig
+
+    suffix = os.path.basename(build.PY_LIB)[len("_paged_fast"):]
+    assert suffix == sysconfig.get_config_var("EXT_SUFFIX") and suffix in importlib.machinery.EXTENSION_SUFFIXES
+    assert suffix not in (".so", ".abi3.so")
+
+
 def test_paged_loads_without_the_module():
     """The checks and the refusals in Python serve where the module is missing."""
     pytest.importorskip("torch")
