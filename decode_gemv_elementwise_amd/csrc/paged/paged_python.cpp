@@ -119,7 +119,15 @@ const void *rows_of(Args &a, int i, at::ScalarType type, int64_t tokens, int64_t
     return t->data_ptr();
 }
 
-PyObject *answer(int status) { return PyLong_FromLong(status); }
+// A library call's status, with the interpreter free for other threads meanwhile: a
+// launch waits where the stream's queue is full.  The caller holds the tensors.
+template <class F> PyObject *answer(F call)
+{
+    PyThreadState *state = PyEval_SaveThread();
+    const int status = call();
+    PyEval_RestoreThread(state);
+    return PyLong_FromLong(status);
+}
 
 PyObject *none() { Py_RETURN_NONE; }
 
@@ -150,8 +158,11 @@ PyObject *slots(PyObject *, PyObject *const *args, Py_ssize_t n)
     Table t;
     if (!a.ok || !table_of(a, 4, requests, &t))
         return none();
-    return answer(call_slots(cached, fresh, requests, free_pages, THPVariable_Unpack(args[2]).size(0), page, t.p, t.width,
-                             t.stride, tokens, query_start, kv_len, request, positions, map, used, stream));
+    const int64_t num_free = THPVariable_Unpack(args[2]).size(0);
+    return answer([&] {
+        return call_slots(cached, fresh, requests, free_pages, num_free, page, t.p, t.width, t.stride, tokens, query_start,
+                          kv_len, request, positions, map, used, stream);
+    });
 }
 
 // (q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache, axis, style, device, stream)
@@ -184,9 +195,13 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
     void *stream = a.address(12);
     if (!a.ok || style > 1)
         return none();
-    return answer(call_append(qp, kp, vp, type_code(q->scalar_type()), tokens, q_heads, qs, ks, vs,
-                              static_cast<const int32_t *>(pos->data_ptr()), axes, axis, inv, 2 * half, (int)style, map,
-                              out->data_ptr(), &c, stream));
+    const int type = type_code(q->scalar_type());
+    const auto *positions = static_cast<const int32_t *>(pos->data_ptr());
+    void *q_out = out->data_ptr();
+    return answer([&] {
+        return call_append(qp, kp, vp, type, tokens, q_heads, qs, ks, vs, positions, axes, axis, inv, 2 * half, (int)style,
+                           map, q_out, &c, stream);
+    });
 }
 
 // (q, k_cache, v_cache, block_table, query_start, kv_len, scale, dst, workspace, window, sinks, device, stream)
@@ -211,10 +226,16 @@ PyObject *attn(PyObject *, PyObject *const *args, Py_ssize_t n)
     Table t;
     if (!a.ok || !table_of(a, 3, requests, &t))
         return none();
-    return answer(call_attn(q->data_ptr(), q->stride(0), q->stride(1), &c, t.p, t.width, t.stride, query_start, kv_len,
-                            requests, q->size(0), q->size(1), (float)PyFloat_AS_DOUBLE(args[6]), window, sinks,
-                            dst->data_ptr(), type_code(dst->scalar_type()), dst->stride(0), dst->stride(1),
-                            work ? work->data_ptr() : nullptr, work ? (int64_t)work->nbytes() : 0, stream));
+    const float scale = (float)PyFloat_AS_DOUBLE(args[6]);
+    const void *qp = q->data_ptr();
+    void *out = dst->data_ptr(), *scratch = work ? work->data_ptr() : nullptr;
+    const int64_t qs[2] = {q->stride(0), q->stride(1)}, os[2] = {dst->stride(0), dst->stride(1)};
+    const int64_t tokens = q->size(0), q_heads = q->size(1), bytes = work ? (int64_t)work->nbytes() : 0;
+    const int type = type_code(dst->scalar_type());
+    return answer([&] {
+        return call_attn(qp, qs[0], qs[1], &c, t.p, t.width, t.stride, query_start, kv_len, requests, tokens, q_heads, scale,
+                         window, sinks, out, type, os[0], os[1], scratch, bytes, stream);
+    });
 }
 
 // (address of gemv_paged_slots, of gemv_paged_append, of gemv_paged_attn): the library that paged.py has loaded
