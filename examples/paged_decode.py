@@ -29,7 +29,7 @@ class Block:
                  sinks=0, seed=0):
         rng = np.random.default_rng(seed)
         self.hidden, self.heads, self.kv_heads, self.dim, self.page = hidden, heads, kv_heads, dim, page
-        self.window, self.sinks = window, sinks
+        self.window, self.sinks, self.longest = window, sinks, longest
         self.rows = (heads + 2 * kv_heads) * dim
         self.w_qkv = synth.random_weights(rng, "bf16", self.rows, hidden)
         self.w_out = synth.random_weights(rng, "bf16", hidden, heads * dim)
@@ -66,12 +66,16 @@ class Block:
                                  add_operand=self.x, dst=self.y)
 
     def step(self, x, fresh, graph=True):
-        """x: [tokens, hidden], the requests' new tokens in their order; fresh: how many each has.  Returns [tokens, hidden]."""
+        """x: [tokens, hidden], the requests' new tokens in their order; fresh: how many each has.  Returns [tokens, hidden].
+        A step that needs more pages than are free, or takes a request past ``longest``, is refused before it takes any."""
         n = sum(fresh)
         assert x.shape == (n, self.hidden) and 0 < n <= COLUMNS and len(fresh) == len(self.lengths)
         need = sum(-(-(c + f) // self.page) - -(-c // self.page) for c, f in zip(self.lengths, fresh))
+        if max(c + f for c, f in zip(self.lengths, fresh)) > self.longest:
+            raise ValueError(f"a request would be longer than {self.longest} tokens")
+        if need > len(self.pool):
+            raise ValueError(f"{need} pages needed, {len(self.pool)} free")
         taken, self.pool = self.pool[:need], self.pool[need:]
-        assert len(taken) == need, "no free pages"
         self.x[:n].copy_(x)
         self.cached.copy_(torch.tensor(self.lengths, dtype=torch.int32))
         self.fresh.copy_(torch.tensor(fresh, dtype=torch.int32))
