@@ -14,9 +14,14 @@
 //
 // Memory-bound where the keys are many: 64 requests of up to 16384 keys (2.19 GB, 32
 // query and 8 key/value heads of 128) take 410 us, 5.34 TB/s; one over 131072 keys
-// 104 us, 5.15 TB/s.  Every wave has 16 KB on its way all the time: a block's k and
-// v are asked for one round ahead (409 us against 416 without), its page ids two.
-// Where they are few it is latency: one token over 4099 keys 15.6 us.
+// 104 to 108 us, 4.95 to 5.15 TB/s.  With heads of 128 every wave has 16 KB on its way
+// all the time (8 with heads of 64): a block's k and v are asked for one round ahead
+// (409 us against 416 without), its page ids two.  Heads of 256 have no registers for
+// that: 64 requests of up to 8192 keys (2.2 GB) take 406 us all the same, 5.4 TB/s.
+// Where the keys are few it is latency: one token over 4099 keys 15.6 us on the GPU.
+//
+// The weights are rounded to 16 bits for the product with v, as the matrix cores take
+// them; for a float32 result they go as two pieces (17.9 us and 412 us of the above).
 #pragma once
 
 #include "paged_attn_device.h"
