@@ -107,6 +107,8 @@ def _cache_of(k_cache, v_cache, device):
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"k_cache and v_cache must be [pages, page_size, heads, dim] alike, got {tuple(shape)} and "
                          f"{tuple(v_cache.shape)}")
+    if max(shape[1:]) >= 2 ** 31:
+        raise ValueError(f"page_size, heads and dim of a cache must be below 2^31, got {tuple(shape)}")
     if v_cache.dtype != k_cache.dtype or k_cache.dtype not in TYPES:
         raise TypeError(f"k_cache and v_cache must be float16 or bfloat16 alike, got {k_cache.dtype} and {v_cache.dtype}")
     if ks[3] != 1 or vs[3] != 1:

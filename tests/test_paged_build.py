@@ -74,3 +74,20 @@ except TypeError as e:
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.strip() == "refused"
+
+
+def test_cache_sizes_past_32_bits_are_refused():
+    """The C structure's sizes are 32 bits wide: a larger one must not come out as another."""
+    torch = pytest.importorskip("torch")
+    from decode_gemv_elementwise_amd import paged
+
+    if not os.path.exists(build.LIB):  # pragma: no cover - the build step makes it
+        pytest.skip("the library is not built")
+    paged.load()
+    dev = torch.device("meta")
+    for shape in ((1, 2 ** 32 + 16, 1, 8), (1, 16, 2 ** 32 + 1, 8), (1, 1, 1, 2 ** 32 + 64)):
+        t = torch.empty(shape, dtype=torch.float16, device=dev)
+        with pytest.raises(ValueError, match="2\\^31"):
+            paged._cache_of(t, t, dev)
+    t = torch.empty((2 ** 20, 16, 8, 128), dtype=torch.float16, device=dev)
+    assert paged._cache_of(t, t, dev).num_pages == 2 ** 20
