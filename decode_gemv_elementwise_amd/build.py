@@ -28,7 +28,9 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = [os.path.join(CSRC, "gemv_kernels.hip"), os.path.join(CSRC, "gemv_cols.hip"),
            os.path.join(CSRC, "gemv_validate.cpp"), os.path.join(CSRC, "gemv_fwht.hip"),
            os.path.join(CSRC, "gemv_mfma.hip"), *(os.path.join(CSRC, "paged", f) for f in (
-               "paged_validate.cpp", "paged_slots.hip", "paged_append.hip", "paged_attn.hip"))]
+               "paged_attn.hip", "paged8_attn_256.hip", "paged8_attn_128.hip", "paged8_attn_64.hip", "paged8_attn.hip",
+               "paged_validate.cpp", "paged_slots.hip", "paged_append.hip", "paged8_validate.cpp", "paged8_append.hip",
+               "paged8_read.hip"))]
 PROBE_SOURCES = [os.path.join(CSRC, "hbm_probe.hip")]
 CPU_SOURCE = os.path.join(HERE, "cpu", "cpu_fused.c")
 CPU_LIB = os.path.join(HERE, "libcpu_fused.so")

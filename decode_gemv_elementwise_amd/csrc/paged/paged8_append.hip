@@ -1,0 +1,531 @@
+// Rotary positions and the quantising write into a paged cache of 8-bit codes
+// (gemv_paged8_append).
+//
+// Tokens of one call in one block of a page share its scale, so they form a run that one
+// workgroup takes: it finds the runs that begin within its few tokens from the slots
+// alone.  A wave holds some tokens of a run whole, a lane 16 values of one of them (for
+// halves 8 and their 8 partners), turned by angles that it forms once for all its heads.
+// Largest size, scale and codes then come from registers: k and v are read once and
+// written once.  Where a run needs several waves, they exchange the largest size through
+// LDS.  Codes that lie in a block already are only touched where its scale grows.
+//
+// A size is compared by its bits: of floats from 0 up they are ordered like whole
+// numbers, infinities and NaN above all others.
+//
+// Memory-bound where the tokens are many, latency-bound where they are few.
+#include "paged8_device.h"
+#include "rotary.h"
+
+namespace gemv {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr int64_t kMostGroups = 1 << 29; // workgroups of either part, where larger shares can see to it
+
+struct Append8Args {
+    const void *src[3]; // q, k, v
+    int64_t src_stride[3];
+    const int32_t *positions, *axis, *slots;
+    const float *inv_freq;
+    void *q_out;
+    uint8_t *codes[2], *scales[2]; // k, v
+    int64_t c_stride[2][3], s_stride[2][3];
+    int32_t tokens, axes, q_heads, heads, dim, half; // half = rot / 2
+    int32_t num_slots;
+    int32_t pairs, e4m3, bf;     // pairing by neighbours; the codes; q_out's type
+    FastDiv page, block;
+    FastDiv items;               // lanes that a token's head takes
+    FastDiv q_shares, kv_shares; // workgroups that share one stretch's heads
+    int32_t stretch;             // tokens in which a workgroup looks for runs
+    int32_t q_share, kv_share;   // heads of a workgroup
+    int32_t kv_groups, groups;   // workgroups for k and v, and all
+};
+
+// Sixteen values of a row: eight from lo on and eight from hi on, as floats.
+template <class S> __device__ __forceinline__ void load16(const S *row, int lo, int hi, float *x)
+{
+    if constexpr (sizeof(S) == 4) {
+        const f32x4 v[4] = {*reinterpret_cast<const f32x4 *>(row + lo), *reinterpret_cast<const f32x4 *>(row + lo + 4),
+                            *reinterpret_cast<const f32x4 *>(row + hi), *reinterpret_cast<const f32x4 *>(row + hi + 4)};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i] = v[i / 4][i % 4];
+    } else {
+        typedef S s8 __attribute__((ext_vector_type(8)));
+        const s8 a = *reinterpret_cast<const s8 *>(row + lo), b = *reinterpret_cast<const s8 *>(row + hi);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = (float)a[i];
+            x[8 + i] = (float)b[i];
+        }
+    }
+}
+
+// Where a lane's sixteen values lie in a row of q or k.  Pair 8 item + e is values
+// (2 e, 2 e + 1) of them, or (e, 8 + e) for halves.
+struct Place {
+    int lo, hi;
+};
+__device__ __forceinline__ Place place_of(const Append8Args &a, int item)
+{
+    if (a.pairs)
+        return Place{16 * item, 16 * item + 8};
+    if (8 * item < a.half)
+        return Place{8 * item, a.half + 8 * item};
+    const int lo = 2 * a.half + 16 * (item - a.half / 8);
+    return Place{lo, lo + 8};
+}
+
+__device__ __forceinline__ float2 turn_at(const Append8Args &a, int t, int pair)
+{
+    const int ax = a.axis ? a.axis[pair] : 0;
+    return (unsigned)ax < (unsigned)a.axes ? turn_of(a.positions[(int64_t)ax * a.tokens + t], a.inv_freq[pair])
+                                           : float2{1.0f, 0.0f};
+}
+
+// The turns of a lane's eight pairs; pairs past rot are not turned.
+__device__ __forceinline__ void turns_of(const Append8Args &a, int t, int item, float2 *turn)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        turn[e] = 8 * item + e < a.half ? turn_at(a, t, 8 * item + e) : float2{1.0f, 0.0f};
+}
+
+__device__ __forceinline__ void turn_pair(float &x, float &y, float2 cs)
+{
+    const float nx = fmaf(x, cs.x, -(y * cs.y)), ny = fmaf(y, cs.x, x * cs.y);
+    x = nx;
+    y = ny;
+}
+
+// Turns a lane's values.  What is not turned stays as it is, infinities among it.
+__device__ __forceinline__ void turn16(const Append8Args &a, int item, const float2 *turn, float *x)
+{
+    if (a.pairs) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (8 * item + e < a.half)
+                turn_pair(x[2 * e], x[2 * e + 1], turn[e]);
+    } else if (8 * item < a.half) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            turn_pair(x[e], x[8 + e], turn[e]);
+    }
+}
+
+__device__ __forceinline__ void store16(const Append8Args &a, uint16_t *row, Place p, const float *x)
+{
+    u32x4 lo, hi;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = a.bf ? pack2<true>(x[2 * i], x[2 * i + 1]) : pack2<false>(x[2 * i], x[2 * i + 1]);
+        hi[i] = a.bf ? pack2<true>(x[8 + 2 * i], x[9 + 2 * i]) : pack2<false>(x[8 + 2 * i], x[9 + 2 * i]);
+    }
+    *reinterpret_cast<u32x4 *>(row + p.lo) = lo;
+    *reinterpret_cast<u32x4 *>(row + p.hi) = hi;
+}
+
+// Four values times 2^(127 - b) as codes.  Within the codes' range, so an e4m3 needs no
+// limit, and a whole number is the low byte of its sum with 1.5 2^23, rounded to even.
+__device__ __forceinline__ uint32_t codes4(bool e4m3, const float *x, float inv)
+{
+    if (e4m3) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inv, x[1] * inv, 0, false);
+        return __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inv, x[3] * inv, lo, true);
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = __builtin_bit_cast(uint32_t, fmaf(x[i], inv, 12582912.0f));
+    const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(w[3], w[2], 0x04000c0cu);
+    return lo | hi;
+}
+
+// The largest over a wave.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = max(v, dpp<0x111, 0xf>(v));
+    v = max(v, dpp<0x112, 0xf>(v));
+    v = max(v, dpp<0x114, 0xf>(v));
+    v = max(v, dpp<0x118, 0xf>(v));
+    v = max(v, dpp<0x142, 0xa>(v));
+    v = max(v, dpp<0x143, 0xc>(v));
+    return __builtin_amdgcn_readlane(v, kWave - 1);
+}
+
+// The scale's byte for a largest size (its bits).  127 is 1.984375 2^6, 448 is 1.75 2^8.
+__device__ __forceinline__ int byte_of(bool e4m3, uint32_t bits)
+{
+    if (bits >= 0x7f800000u)
+        return 255;
+    const int e = bits >> 23, m = bits & 0x7fffffu;
+    return max(1, e4m3 ? e - 8 + (m > 0x600000) : e - 6 + (m > 0x7e0000));
+}
+
+// 2^(127 - b); a block that is NaN needs no codes.
+__device__ __forceinline__ float inverse_of(int b) { return b == 255 ? 0.0f : __builtin_bit_cast(float, (uint32_t)(254 - b) << 23); }
+
+// Tokens [first, first + n) of one block.
+struct Run {
+    int first, n, block;
+    bool begun;    // the block's first place is among theirs
+    bool straight; // their places follow one another
+};
+
+// The block of token t's slot; -1 where it has none, also past either end (t is -1 there or passes 2^31).
+__device__ __forceinline__ int block_at(const Append8Args &a, uint32_t t)
+{
+    const int slot = t < (uint32_t)a.tokens ? a.slots[t] : -1;
+    return slot >= 0 && slot < a.num_slots ? (int)div_by(a.block, slot) : -1;
+}
+
+// The run that begins at token t (which does begin one).  Whole waves only.
+__device__ __forceinline__ Run run_at(const Append8Args &a, int t, int lane)
+{
+    Run r{t, 0, __builtin_amdgcn_readfirstlane(block_at(a, t)), false, true};
+    const int start = a.slots[t];
+    for (;;) {
+        const uint32_t i = (uint32_t)t + r.n + lane;
+        const uint64_t other = __ballot(block_at(a, i) != r.block);
+        const int more = other ? __builtin_ctzll(other) : kWave;
+        const int slot = lane < more ? a.slots[i] : -1;
+        r.begun = r.begun || __any(lane < more && slot == r.block * (int)a.block.d);
+        r.straight = r.straight && !__any(lane < more && slot != start + r.n + lane);
+        r.n += more;
+        if (more < kWave)
+            return r;
+    }
+}
+
+// Whether one of the run's tokens has place p of the block.
+__device__ __forceinline__ bool has_place(const Append8Args &a, const Run &r, int p)
+{
+    const int slot = r.block * (int)a.block.d + p;
+    if (r.straight) {
+        const int start = a.slots[r.first];
+        return slot >= start && slot < start + r.n;
+    }
+    for (int i = 0; i < r.n; ++i)
+        if (a.slots[r.first + i] == slot)
+            return true;
+    return false;
+}
+
+// A head's codes and scale of a block.
+struct Target {
+    uint8_t *codes;
+    uint8_t *scale;
+    int64_t place; // stride of places
+};
+__device__ __forceinline__ Target target_of(const Append8Args &a, int block, int v, int head)
+{
+    const uint32_t first = (uint32_t)block * a.block.d, id = div_by(a.page, first), in = first - id * a.page.d;
+    const int64_t *c = a.c_stride[v], *s = a.s_stride[v];
+    return Target{a.codes[v] + id * c[0] + in * c[1] + head * c[2],
+                  a.scales[v] + id * s[0] + div_by(a.block, in) * s[1] + head * s[2], c[1]};
+}
+
+// What a block holds beside the run, from scale byte `old` to the larger b, by `threads`
+// threads of which this is the i-th.  16 codes at a time.
+__device__ __forceinline__ void rescale(const Append8Args &a, const Run &r, const Target &to, int old, int b, int i, int threads)
+{
+    const int pieces = a.dim / 16;
+    const float f = __builtin_bit_cast(float, (uint32_t)max(127 + old - b, 0) << 23); // a step so small leaves 0 either way
+    for (int at = i; at < (int)a.block.d * pieces; at += threads) {
+        const int p = at / pieces;
+        if (has_place(a, r, p))
+            continue;
+        u32x4 *const w = reinterpret_cast<u32x4 *>(to.codes + p * to.place + 16 * (at - p * pieces));
+        u32x4 x = *w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f32x4 y = a.e4m3 ? floats4<GEMV_KV_E4M3>(x[e], 1.0f) : floats4<GEMV_KV_INT8>(x[e], 1.0f);
+            const float z[4] = {y[0], y[1], y[2], y[3]};
+            x[e] = codes4(a.e4m3, z, f);
+        }
+        *w = x;
+    }
+}
+
+// A grid's x counts its threads in 32 bits, so past 2^16 workgroups y goes on.
+constexpr int64_t kGroupsX = 65536;
+__device__ __forceinline__ int group_here() { return blockIdx.y * kGroupsX + blockIdx.x; }
+
+// The workgroups of k and v: stretches of tokens times shares of the 2 heads rows.
+// one(run, item of the rows, first, step): the work on a run.
+template <class F> __device__ __forceinline__ void each_run(const Append8Args &a, int group, F one)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const int at = div_by(a.kv_shares, group), share = group - at * a.kv_shares.d;
+    const uint32_t t0 = (uint32_t)at * a.stretch;
+    // lane i: does a run begin at token t0 + i; a stretch is shorter than a wave
+    const int mine = block_at(a, t0 + lane), before = block_at(a, t0 + lane - 1);
+    uint64_t begins = __ballot(lane < a.stretch && mine >= 0 && mine != before);
+    while (begins) {
+        const int i = __builtin_ctzll(begins);
+        begins &= begins - 1;
+        one(run_at(a, (int)(t0 + i), lane), share);
+    }
+}
+
+// The wide path: 16-byte vectors of whole rows.  PP: tokens that a lane holds values of;
+// a run of more than four waves hold (two tokens of one slot are in it) is taken in parts.
+template <class S, int PP> __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
+{
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int sub = div_by(a.items, lane), item = lane - sub * a.items.d;
+    const int per = kWave / (int)a.items.d; // tokens of a wave at a time
+    const Place kq = place_of(a, item), plain{16 * item, 16 * item + 8};
+
+    if (group_here() >= a.groups)
+        return;
+    if (group_here() >= a.kv_groups) { // q
+        const int group = group_here() - a.kv_groups, at = div_by(a.q_shares, group), share = group - at * a.q_shares.d;
+        const uint32_t t = ((uint32_t)at * kWaves + wave) * per + sub;
+        if (sub >= per || t >= (uint32_t)a.tokens)
+            return;
+        const int h1 = min((share + 1) * a.q_share, a.q_heads);
+        float2 turn[8];
+        turns_of(a, t, item, turn);
+        const S *row = static_cast<const S *>(a.src[0]) + (int64_t)t * a.src_stride[0];
+        uint16_t *out = static_cast<uint16_t *>(a.q_out) + (int64_t)t * a.q_heads * a.dim;
+        for (int h = share * a.q_share; h < h1; ++h) {
+            float x[16];
+            load16(row + h * a.dim, kq.lo, kq.hi, x);
+            turn16(a, item, turn, x);
+            store16(a, out + h * a.dim, kq, x);
+        }
+        return;
+    }
+
+    __shared__ uint32_t largest[2][kWaves];
+    int turned = 0; // which half of `largest`
+    each_run(a, group_here(), [&](Run r, int share) {
+        const int most = kWaves * PP * per;
+        for (int left = r.n; left > 0; left -= most) {
+            const int from = r.first + (r.n - left), n = min(left, most);
+            // waves of a team, which takes a head together
+            const int passes = (n + per - 1) / per, team = passes == 1 ? 1 : passes == 2 ? 2 : 4, me = wave & (team - 1);
+            uint32_t t[PP];
+            bool live[PP];
+            float2 turn[PP][8];
+            bool formed = false;
+#pragma unroll
+            for (int i = 0; i < PP; ++i) {
+                const int off = (i * team + me) * per + sub;
+                t[i] = (uint32_t)from + off;
+                live[i] = sub < per && off < n;
+            }
+            const int last = min((share + 1) * a.kv_share, 2 * a.heads);
+            for (int row0 = share * a.kv_share; row0 < last; row0 += kWaves / team) {
+                const int row = row0 + wave / team;
+                const bool on = row < last;
+                const int v = row >= a.heads, head = v ? row - a.heads : row;
+                const Place p = v ? plain : kq;
+                float x[PP][16];
+                uint32_t top = 0;
+                Target to{};
+                int old = 0;
+                if (on) {
+                    to = target_of(a, r.block, v, head);
+                    if (!r.begun || from != r.first)
+                        old = *to.scale;
+#pragma unroll
+                    for (int i = 0; i < PP; ++i)
+                        if (live[i])
+                            load16(static_cast<const S *>(a.src[1 + v]) + (int64_t)t[i] * a.src_stride[1 + v] + head * a.dim, p.lo, p.hi,
+                                   x[i]);
+                    if (!v && !formed) {
+#pragma unroll
+                        for (int i = 0; i < PP; ++i)
+                            if (live[i])
+                                turns_of(a, t[i], item, turn[i]);
+                        formed = true;
+                    }
+#pragma unroll
+                    for (int i = 0; i < PP; ++i)
+                        if (live[i]) {
+                            if (!v)
+                                turn16(a, item, turn[i], x[i]);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                top = max(top, __builtin_bit_cast(uint32_t, x[i][e]) & 0x7fffffffu);
+                        }
+                    top = wave_max(top);
+                }
+                if (team > 1) {
+                    if (lane == 0)
+                        largest[turned][wave] = top;
+                    __syncthreads();
+                    for (int w = 0; w < team; ++w)
+                        top = max(top, largest[turned][wave - me + w]);
+                    turned ^= 1; // the next head's go where none reads any more
+                }
+                if (!on)
+                    continue;
+                const bool begun = r.begun && from == r.first;
+                const int b = begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
+                if (!begun && b > old && b < 255)
+                    rescale(a, r, to, old, b, me * kWave + lane, team * kWave);
+                const float inv = inverse_of(b);
+                if (me == 0 && lane == 0)
+                    *to.scale = (uint8_t)b;
+#pragma unroll
+                for (int i = 0; i < PP; ++i)
+                    if (live[i]) {
+                        uint8_t *out = to.codes + (a.slots[t[i]] - r.block * (int)a.block.d) * to.place;
+                        *reinterpret_cast<u32x2 *>(out + p.lo) = u32x2{codes4(a.e4m3, x[i], inv), codes4(a.e4m3, x[i] + 4, inv)};
+                        *reinterpret_cast<u32x2 *>(out + p.hi) =
+                            u32x2{codes4(a.e4m3, x[i] + 8, inv), codes4(a.e4m3, x[i] + 12, inv)};
+                    }
+            }
+            __syncthreads(); // a further part's and a further run's reads of this one's writes; `largest`
+        }
+    });
+}
+
+// Any alignment, any even rot, any block: a thread takes one value at a time, twice.
+template <class S> __global__ __launch_bounds__(kThreads) void paged8_append_generic_kernel(Append8Args a)
+{
+    const auto value = [&](int which, int t, int head, int e) {
+        const S *row = static_cast<const S *>(a.src[which]) + (int64_t)t * a.src_stride[which] + head * a.dim;
+        if (which == 2 || e >= 2 * a.half)
+            return (float)row[e];
+        const int pair = a.pairs ? e / 2 : e < a.half ? e : e - a.half;
+        const int lo = a.pairs ? 2 * pair : pair, hi = a.pairs ? lo + 1 : lo + a.half;
+        float x = (float)row[lo], y = (float)row[hi];
+        turn_pair(x, y, turn_at(a, t, pair));
+        return e == lo ? x : y;
+    };
+    if (group_here() >= a.groups)
+        return;
+    if (group_here() >= a.kv_groups) { // q: a workgroup for a token's share of heads
+        const int group = group_here() - a.kv_groups, t = div_by(a.q_shares, group), share = group - t * a.q_shares.d;
+        const int h0 = share * a.q_share, h1 = min(h0 + a.q_share, a.q_heads);
+        uint16_t *out = static_cast<uint16_t *>(a.q_out) + (int64_t)t * a.q_heads * a.dim;
+        for (int i = h0 * a.dim + threadIdx.x; i < h1 * a.dim; i += kThreads) {
+            const int h = i / a.dim;
+            const float x = value(0, t, h, i - h * a.dim);
+            out[i] = (uint16_t)(a.bf ? pack2<true>(x, 0.0f) : pack2<false>(x, 0.0f));
+        }
+        return;
+    }
+    __shared__ uint32_t largest[kWaves];
+    each_run(a, group_here(), [&](Run r, int share) {
+        const int last = min((share + 1) * a.kv_share, 2 * a.heads);
+        for (int row = share * a.kv_share; row < last; ++row) {
+            const int v = row >= a.heads, head = v ? row - a.heads : row;
+            const Target to = target_of(a, r.block, v, head);
+            const int old = *to.scale;
+            uint32_t top = 0;
+            for (int64_t i = threadIdx.x; i < (int64_t)r.n * a.dim; i += kThreads) {
+                const int at = (int)(i / a.dim);
+                top = max(top, __builtin_bit_cast(uint32_t, value(1 + v, r.first + at, head, (int)(i - (int64_t)at * a.dim))) & 0x7fffffffu);
+            }
+            top = wave_max(top);
+            if ((threadIdx.x & (kWave - 1)) == 0)
+                largest[threadIdx.x / kWave] = top;
+            __syncthreads(); // and the scale is read by all
+            for (int w = 0; w < kWaves; ++w)
+                top = max(top, largest[w]);
+            const int b = r.begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
+            if (!r.begun && b > old && b < 255)
+                rescale(a, r, to, old, b, threadIdx.x, kThreads);
+            const float inv = inverse_of(b);
+            if (threadIdx.x == 0)
+                *to.scale = (uint8_t)b;
+            for (int64_t i = threadIdx.x; i < (int64_t)r.n * a.dim; i += kThreads) {
+                const int at = (int)(i / a.dim), e = (int)(i - (int64_t)at * a.dim);
+                const float x[4] = {value(1 + v, r.first + at, head, e), 0.0f, 0.0f, 0.0f};
+                to.codes[(a.slots[r.first + at] - r.block * (int)a.block.d) * to.place + e] = (uint8_t)codes4(a.e4m3, x, inv);
+            }
+            __syncthreads(); // `largest` is free, and what this run wrote is there for the next
+        }
+    });
+}
+
+template <class S> const void *kernel_of(int passes)
+{
+    return passes == 1   ? reinterpret_cast<const void *>(&paged8_append_kernel<S, 1>)
+           : passes == 2 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, 2>)
+           : passes == 4 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, 4>)
+                         : reinterpret_cast<const void *>(&paged8_append_generic_kernel<S>);
+}
+
+} // namespace
+} // namespace gemv
+
+extern "C" int gemv_paged8_append(const void *q, const void *k, const void *v, int src_type, int64_t tokens,
+                                  int64_t q_heads, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  const int32_t *positions, int64_t axes, const int32_t *axis, const float *inv_freq,
+                                  int64_t rot, int style, const int32_t *slots, void *q_out, int q_out_type,
+                                  const gemv_kv_cache8 *cache, void *hip_stream)
+{
+    const int st = gemv::validate_append8(q, k, v, src_type, tokens, q_heads, q_stride, k_stride, v_stride, positions,
+                                          axes, axis, inv_freq, rot, style, slots, q_out, q_out_type, cache);
+    if (st != GEMV_OK)
+        return st;
+    if (tokens == 0)
+        return gemv::finish_launch((int)hipSuccess);
+    gemv::Append8Args a{};
+    a.src[0] = q, a.src[1] = k, a.src[2] = v;
+    a.src_stride[0] = q_stride, a.src_stride[1] = k_stride, a.src_stride[2] = v_stride;
+    a.positions = positions, a.axis = axis, a.slots = slots, a.inv_freq = inv_freq, a.q_out = q_out;
+    a.codes[0] = static_cast<uint8_t *>(cache->k), a.codes[1] = static_cast<uint8_t *>(cache->v);
+    a.scales[0] = cache->k_scale, a.scales[1] = cache->v_scale;
+    for (int d = 0; d < 3; ++d) {
+        a.c_stride[0][d] = cache->k_stride[d], a.c_stride[1][d] = cache->v_stride[d];
+        a.s_stride[0][d] = cache->ks_stride[d], a.s_stride[1][d] = cache->vs_stride[d];
+    }
+    a.tokens = (int)tokens, a.axes = (int)axes, a.q_heads = (int)q_heads, a.heads = cache->heads, a.dim = cache->dim;
+    a.half = (int)(rot / 2), a.pairs = style == GEMV_ROPE_PAIRS;
+    a.num_slots = (int)(cache->num_pages * cache->page_size);
+    a.e4m3 = cache->code == GEMV_KV_E4M3, a.bf = q_out_type == GEMV_W_BF16;
+    a.page = gemv::fast_div(cache->page_size), a.block = gemv::fast_div(cache->block);
+
+    // wide: 16-byte vectors of whole rows.  The cache and q_out always allow them
+    // (checked strides and alignment); the rows of q, k and v and rot may not.
+    const int64_t size = src_type == GEMV_W_F32 ? 4 : 2;
+    bool wide = rot % (a.pairs ? 8 : 16) == 0;
+    for (int i = 0; i < 3; ++i)
+        wide = wide && reinterpret_cast<uintptr_t>(a.src[i]) % 16 == 0 && a.src_stride[i] * size % 16 == 0;
+    const int items = cache->dim / 16, per = gemv::kWave / items; // lanes of a token's head, tokens of a wave at a time
+    a.items = gemv::fast_div(items);
+    const int64_t need = (cache->block + gemv::kWaves * per - 1) / (gemv::kWaves * per); // passes of a whole block
+    const int passes = !wide || need > 4 ? 0 : need > 2 ? 4 : (int)need;
+
+    // Enough workgroups to fill the card: rows of k and v are shared out four at a time,
+    // and from some 8000 workgroups on each looks for runs in more tokens instead.
+    const int64_t rows = 2 * (int64_t)a.heads;
+    int64_t kv_share = 4, kv_shares = (rows + kv_share - 1) / kv_share;
+    int64_t stretch = (tokens * kv_shares + 8191) / 8192;
+    const int64_t most = cache->block < 32 ? cache->block : 32;
+    stretch = stretch < most ? stretch : most;
+    const int64_t stretches = (tokens + stretch - 1) / stretch;
+    while (stretches * kv_shares > gemv::kMostGroups && kv_share < rows) {
+        kv_share *= 2;
+        kv_shares = (rows + kv_share - 1) / kv_share;
+    }
+    a.stretch = (int)stretch, a.kv_share = (int)kv_share;
+    const int64_t kv_groups = stretches * kv_shares;
+    const int64_t together = passes ? gemv::kWaves * per : 1; // tokens of a q workgroup
+    const int64_t q_groups = (tokens + together - 1) / together;
+    int64_t q_share = q_groups * q_heads / 4096;
+    q_share = q_share < 1 ? 1 : q_share < 8 ? q_share : 8;
+    while (q_groups * ((q_heads + q_share - 1) / q_share) > gemv::kMostGroups && q_share < q_heads)
+        q_share *= 2;
+    const int64_t q_shares = (q_heads + q_share - 1) / q_share, groups = kv_groups + q_groups * q_shares;
+    if (groups > INT_MAX) // rows of a stride of 0 for more tokens and heads than any memory holds
+        return GEMV_E_DIM;
+    a.q_share = (int)q_share;
+    a.q_shares = gemv::fast_div(q_shares), a.kv_shares = gemv::fast_div(kv_shares);
+    a.kv_groups = (int)kv_groups, a.groups = (int)groups;
+    const void *fn = src_type == GEMV_W_F32   ? gemv::kernel_of<float>(passes)
+                     : src_type == GEMV_W_F16 ? gemv::kernel_of<_Float16>(passes)
+                                              : gemv::kernel_of<__bf16>(passes);
+    void *args[] = {&a};
+    const int64_t x = groups < gemv::kGroupsX ? groups : gemv::kGroupsX;
+    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)x, (unsigned)((groups + x - 1) / x)), dim3(gemv::kThreads), args, 0,
+                                         static_cast<hipStream_t>(hip_stream));
+    return gemv::finish_launch((int)e);
+}

@@ -1,0 +1,89 @@
+// gemv_paged8_attn: what the host works out for the attention over a cache of 8-bit codes.
+#include <cfloat>
+#include <cmath>
+
+#include "paged8_attn_device.h"
+
+namespace gemv {
+namespace {
+
+// Which kind of row tile a call takes.  The host knows the counts of tokens and requests
+// and no lengths: tiles of few rows where a request has one token, or up to 16 rows, on
+// average; but with more tokens than kFewTokens only the first, for a long chunk among
+// them would read its keys again for every 16 rows.
+constexpr int64_t kFewTokens = 256;
+
+bool takes_many(int64_t tokens, int64_t requests, int64_t group)
+{
+    return tokens > requests && (tokens * group > kAttnRows * requests || tokens > kFewTokens);
+}
+
+} // namespace
+} // namespace gemv
+
+extern "C" int gemv_paged8_attn(const void *q, int q_type, int64_t q_token_stride, int64_t q_head_stride,
+                                const gemv_kv_cache8 *cache, const int32_t *block_table, int64_t table_width,
+                                int64_t table_stride, const int32_t *query_start, const int32_t *kv_len,
+                                int64_t requests, int64_t tokens, int64_t q_heads, float scale, int64_t window,
+                                int64_t sinks, void *out, int out_type, int64_t out_token_stride,
+                                int64_t out_head_stride, void *workspace, int64_t workspace_bytes, void *hip_stream)
+{
+    const int st = gemv::validate_attn8(q, q_type, q_token_stride, q_head_stride, cache, block_table, table_width,
+                                        table_stride, query_start, kv_len, requests, tokens, q_heads, scale, window,
+                                        sinks, out, out_type, out_token_stride, out_head_stride, workspace,
+                                        workspace_bytes);
+    if (st != GEMV_OK)
+        return st;
+    if (tokens == 0)
+        return gemv::finish_launch((int)hipSuccess);
+    gemv::Attn8Args a{};
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(cache->k);
+    a.v = static_cast<const uint16_t *>(cache->v);
+    a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
+    a.q_ts = q_token_stride, a.q_hs = q_head_stride, a.o_ts = out_token_stride, a.o_hs = out_head_stride;
+    for (int d = 0; d < 3; ++d) {
+        a.k_stride[d] = (uint32_t)cache->k_stride[d], a.v_stride[d] = (uint32_t)cache->v_stride[d];
+        a.ks_stride[d] = (uint32_t)cache->ks_stride[d], a.vs_stride[d] = (uint32_t)cache->vs_stride[d];
+    }
+    a.table = block_table, a.query_start = query_start, a.kv_len = kv_len, a.table_stride = table_stride;
+    a.out = out;
+    const int64_t room = (workspace_bytes - gemv::kAttnCounters * 4) / 4;
+    a.counters = static_cast<int32_t *>(workspace);
+    a.parts = reinterpret_cast<float *>(a.counters + gemv::kAttnCounters);
+    a.part_room = room < 0 ? 0 : room;
+    a.width = (int)table_width, a.requests = (int)requests, a.tokens = (int)tokens, a.heads = cache->heads;
+    a.group = (int)(q_heads / cache->heads), a.num_pages = (int)cache->num_pages;
+    a.window = (int)window, a.sinks = window > 0 ? (int)sinks : 0;
+    a.reach = table_width * cache->page_size; // a round's last key stays below 2^31
+    a.reach = a.reach < INT_MAX - 63 ? a.reach : INT_MAX - 63;
+    const float s = std::fabs(scale) * 1.44269504088896340736f;
+    a.scale_log2 = s == 0.0f ? 1.0f : std::fmin(s, FLT_MAX);
+    a.q_keep = s == 0.0f ? 0u : ~0u;
+    a.q_flip = scale < 0.0f && s != 0.0f ? 0x80008000u : 0u;
+    a.page = gemv::fast_div(cache->page_size), a.block = gemv::fast_div(cache->block);
+    a.per_group = gemv::fast_div(a.group);
+
+    const bool many = gemv::takes_many(tokens, requests, a.group);
+    const bool runs = cache->block % 8 == 0; // eight keys from a multiple of eight on lie in one page and share a scale
+    const bool f32out = out_type == GEMV_W_F32, bf = q_type == GEMV_W_BF16;
+    const void *fn = cache->dim == 64    ? gemv::paged8_attn_kernel_64(cache->code, bf, f32out, runs, many)
+                     : cache->dim == 128 ? gemv::paged8_attn_kernel_128(cache->code, bf, f32out, runs, many)
+                                         : gemv::paged8_attn_kernel_256(cache->code, bf, f32out, runs, many);
+    // no more workgroups than shares can be: row tiles times the blocks that the
+    // table's width allows
+    const int64_t blocks = (a.reach + gemv::kCostBlock - 1) / gemv::kCostBlock;
+    int64_t tiles = tokens * a.group / gemv::kAttnRows + (requests < tokens ? requests : tokens);
+    tiles = (tiles < tokens * a.group ? tiles : tokens * a.group) * a.heads; // at most tokens * q_heads, below 2^31
+    const int64_t cap = (INT_MAX - 1) / tiles; // of a tile's cost
+    const int64_t start = cache->dim == 64 ? 16 : 8;
+    a.tile_cost = (int)(start <= cap / 2 ? start : cap > 1 ? cap / 2 : 1);
+    while (a.tile_cost + (blocks >> a.unit_log2) > cap)
+        ++a.unit_log2;
+    const int64_t most = gemv::kAttnGroups, shares = (blocks + a.tile_cost) / 8 + 1;
+    const int grid = (int)(tiles >= most || shares >= most || tiles * shares >= most ? most : tiles * shares);
+    void *args[] = {&a};
+    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)grid), dim3(gemv::kThreads), args, 0,
+                                         static_cast<hipStream_t>(hip_stream));
+    return gemv::finish_launch((int)e);
+}
