@@ -1,13 +1,16 @@
 // Rotary positions and the quantising write into a paged cache of 8-bit codes
 // (gemv_paged8_append).
 //
-// Tokens of one call in one block of a page share its scale, so they form a run that one
-// workgroup takes: it finds the runs that begin within its few tokens from the slots
-// alone.  A wave holds some tokens of a run whole, a lane 16 values of one of them (for
+// Tokens of one call in one block of a page share its scale, so they form a run, and a
+// run's head is written as one: a wave holds it whole, a lane 16 values of a token (for
 // halves 8 and their 8 partners), turned by angles that it forms once for all its heads.
 // Largest size, scale and codes then come from registers: k and v are read once and
-// written once.  Where a run needs several waves, they exchange the largest size through
-// LDS.  Codes that lie in a block already are only touched where its scale grows.
+// written once, and waves do not wait for one another.  A workgroup finds the runs that
+// begin within its few tokens from the slots alone and deals their heads out to its
+// waves.  A single token is one sixteenth of a wave's values or so: there a wave takes
+// several heads at once.  Blocks of more tokens than a wave holds are taken by four,
+// which exchange the largest size through LDS.  q goes by workgroups of its own, one a
+// token, whose threads share the angles through LDS.
 //
 // A size is compared by its bits: of floats from 0 up they are ordered like whole
 // numbers, infinities and NaN above all others.
@@ -35,40 +38,49 @@ struct Append8Args {
     int32_t pairs, e4m3, bf;     // pairing by neighbours; the codes; q_out's type
     FastDiv page, block;
     FastDiv items;               // lanes that a token's head takes
-    FastDiv q_shares, kv_shares; // workgroups that share one stretch's heads
+    FastDiv q_items;             // items of 16 values that a token's q has
+    FastDiv q_shares, kv_shares; // workgroups that share one token's q, one stretch's k and v
     int32_t stretch;             // tokens in which a workgroup looks for runs
-    int32_t q_share, kv_share;   // heads of a workgroup
+    int32_t q_share, kv_share;   // items of q, rows of k and v of a workgroup
+    int32_t q_tokens;            // tokens of a q workgroup
     int32_t kv_groups, groups;   // workgroups for k and v, and all
 };
 
-// Sixteen values of a row: eight from lo on and eight from hi on, as floats.
-template <class S> __device__ __forceinline__ void load16(const S *row, int lo, int hi, float *x)
-{
-    if constexpr (sizeof(S) == 4) {
-        const f32x4 v[4] = {*reinterpret_cast<const f32x4 *>(row + lo), *reinterpret_cast<const f32x4 *>(row + lo + 4),
-                            *reinterpret_cast<const f32x4 *>(row + hi), *reinterpret_cast<const f32x4 *>(row + hi + 4)};
+// Sixteen values of a row, eight from lo on and eight from hi on, as they lie in memory.
+template <class S> struct Raw16 {
+    u32x4 x[sizeof(S)];
+    __device__ __forceinline__ void load(const S *row, int lo, int hi)
+    {
+        constexpr int N = sizeof(S) / 2;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            x[i] = v[i / 4][i % 4];
-    } else {
-        typedef S s8 __attribute__((ext_vector_type(8)));
-        const s8 a = *reinterpret_cast<const s8 *>(row + lo), b = *reinterpret_cast<const s8 *>(row + hi);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = (float)a[i];
-            x[8 + i] = (float)b[i];
+        for (int i = 0; i < N; ++i) {
+            x[i] = reinterpret_cast<const u32x4 *>(row + lo)[i];
+            x[N + i] = reinterpret_cast<const u32x4 *>(row + hi)[i];
         }
     }
-}
+    __device__ __forceinline__ void widen(float *v) const
+    {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if constexpr (sizeof(S) == 4) {
+                const uint32_t w = x[i / 4][i % 4];
+                v[i] = __builtin_bit_cast(float, w);
+            } else {
+                const uint16_t w = (uint16_t)(x[i / 8][i % 8 / 2] >> (16 * (i % 2)));
+                v[i] = (float)__builtin_bit_cast(S, w);
+            }
+        }
+    }
+};
 
 // Where a lane's sixteen values lie in a row of q or k.  Pair 8 item + e is values
 // (2 e, 2 e + 1) of them, or (e, 8 + e) for halves.
 struct Place {
     int lo, hi;
 };
-__device__ __forceinline__ Place place_of(const Append8Args &a, int item)
+template <bool PAIRS> __device__ __forceinline__ Place place_of(const Append8Args &a, int item)
 {
-    if (a.pairs)
+    if (PAIRS)
         return Place{16 * item, 16 * item + 8};
     if (8 * item < a.half)
         return Place{8 * item, a.half + 8 * item};
@@ -99,9 +111,9 @@ __device__ __forceinline__ void turn_pair(float &x, float &y, float2 cs)
 }
 
 // Turns a lane's values.  What is not turned stays as it is, infinities among it.
-__device__ __forceinline__ void turn16(const Append8Args &a, int item, const float2 *turn, float *x)
+template <bool PAIRS> __device__ __forceinline__ void turn16(const Append8Args &a, int item, const float2 *turn, float *x)
 {
-    if (a.pairs) {
+    if constexpr (PAIRS) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (8 * item + e < a.half)
@@ -168,43 +180,39 @@ __device__ __forceinline__ float inverse_of(int b) { return b == 255 ? 0.0f : __
 // Tokens [first, first + n) of one block.
 struct Run {
     int first, n, block;
+    int slot;      // the first token's
     bool begun;    // the block's first place is among theirs
     bool straight; // their places follow one another
 };
 
-// The block of token t's slot; -1 where it has none, also past either end (t is -1 there or passes 2^31).
-__device__ __forceinline__ int block_at(const Append8Args &a, uint32_t t)
+__device__ __forceinline__ int slot_at(const Append8Args &a, uint32_t t) { return t < (uint32_t)a.tokens ? a.slots[t] : -1; }
+
+// A slot's block; -1 where it is none.
+__device__ __forceinline__ int block_of(const Append8Args &a, int slot)
 {
-    const int slot = t < (uint32_t)a.tokens ? a.slots[t] : -1;
     return slot >= 0 && slot < a.num_slots ? (int)div_by(a.block, slot) : -1;
 }
 
-// The run that begins at token t (which does begin one).  Whole waves only.
-__device__ __forceinline__ Run run_at(const Append8Args &a, int t, int lane)
+// Adds the run's next tokens, at most a wave's: lane i's slot is that of token `at` + i.
+// True where the run may go on behind them.
+__device__ __forceinline__ bool extend(const Append8Args &a, Run &r, uint32_t at, int slot, int lane)
 {
-    Run r{t, 0, __builtin_amdgcn_readfirstlane(block_at(a, t)), false, true};
-    const int start = a.slots[t];
-    for (;;) {
-        const uint32_t i = (uint32_t)t + r.n + lane;
-        const uint64_t other = __ballot(block_at(a, i) != r.block);
-        const int more = other ? __builtin_ctzll(other) : kWave;
-        const int slot = lane < more ? a.slots[i] : -1;
-        r.begun = r.begun || __any(lane < more && slot == r.block * (int)a.block.d);
-        r.straight = r.straight && !__any(lane < more && slot != start + r.n + lane);
-        r.n += more;
-        if (more < kWave)
-            return r;
-    }
+    const int from = (int)((uint32_t)r.first + r.n - at); // lane of the next token
+    const uint64_t other = __ballot(block_of(a, slot) != r.block) & (~0ull << from);
+    const int to = other ? __builtin_ctzll(other) : kWave;
+    const bool mine = lane >= from && lane < to;
+    r.begun = r.begun || __any(mine && slot == r.block * (int)a.block.d);
+    r.straight = r.straight && !__any(mine && (uint32_t)slot - r.slot != at + lane - r.first);
+    r.n += to - from;
+    return to == kWave;
 }
 
 // Whether one of the run's tokens has place p of the block.
 __device__ __forceinline__ bool has_place(const Append8Args &a, const Run &r, int p)
 {
     const int slot = r.block * (int)a.block.d + p;
-    if (r.straight) {
-        const int start = a.slots[r.first];
-        return slot >= start && slot < start + r.n;
-    }
+    if (r.straight)
+        return slot >= r.slot && slot - r.slot < r.n;
     for (int i = 0; i < r.n; ++i)
         if (a.slots[r.first + i] == slot)
             return true;
@@ -252,134 +260,231 @@ constexpr int64_t kGroupsX = 65536;
 __device__ __forceinline__ int group_here() { return blockIdx.y * kGroupsX + blockIdx.x; }
 
 // The workgroups of k and v: stretches of tokens times shares of the 2 heads rows.
-// one(run, item of the rows, first, step): the work on a run.
+// one(run, share): the work on a run.
 template <class F> __device__ __forceinline__ void each_run(const Append8Args &a, int group, F one)
 {
     const int lane = threadIdx.x & (kWave - 1);
     const int at = div_by(a.kv_shares, group), share = group - at * a.kv_shares.d;
     const uint32_t t0 = (uint32_t)at * a.stretch;
     // lane i: does a run begin at token t0 + i; a stretch is shorter than a wave
-    const int mine = block_at(a, t0 + lane), before = block_at(a, t0 + lane - 1);
-    uint64_t begins = __ballot(lane < a.stretch && mine >= 0 && mine != before);
+    const int slot = slot_at(a, t0 + lane), before = slot_at(a, t0 + lane - 1), mine = block_of(a, slot);
+    uint64_t begins = __ballot(lane < a.stretch && mine >= 0 && mine != block_of(a, before));
     while (begins) {
         const int i = __builtin_ctzll(begins);
         begins &= begins - 1;
-        one(run_at(a, (int)(t0 + i), lane), share);
+        Run r{(int)(t0 + i), 0, (int)__builtin_amdgcn_readlane(mine, i), (int)__builtin_amdgcn_readlane(slot, i), false, true};
+        bool more = extend(a, r, t0, slot, lane);
+        while (more) {
+            const uint32_t next = (uint32_t)r.first + r.n;
+            more = extend(a, r, next, slot_at(a, next + lane), lane);
+        }
+        one(r, share);
     }
 }
 
-// The wide path: 16-byte vectors of whole rows.  PP: tokens that a lane holds values of;
-// a run of more than four waves hold (two tokens of one slot are in it) is taken in parts.
-template <class S, int PP> __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
+// q of a few tokens, an item of 16 values a thread; the turns are formed while the first
+// items are on their way.
+template <class S, bool PAIRS> __device__ __forceinline__ void turn_q(const Append8Args &a, int group, float2 *turns)
 {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int sub = div_by(a.items, lane), item = lane - sub * a.items.d;
-    const int per = kWave / (int)a.items.d; // tokens of a wave at a time
-    const Place kq = place_of(a, item), plain{16 * item, 16 * item + 8};
+    const int at = div_by(a.q_shares, group), share = group - at * a.q_shares.d;
+    const uint32_t t0 = (uint32_t)at * a.q_tokens;
+    const int tokens = (int)min((uint32_t)a.q_tokens, (uint32_t)a.tokens - t0), per = min(a.q_share, (int)a.q_items.d - share * a.q_share);
+    bool formed = false;
+    for (int i = threadIdx.x;; i += kThreads) {
+        const bool live = i < tokens * per;
+        Raw16<S> raw;
+        int sub = 0, head = 0, item = 0;
+        Place p{};
+        if (live) {
+            sub = a.q_tokens == 1 ? 0 : i / per;
+            const int in = share * a.q_share + i - sub * per;
+            head = div_by(a.items, in);
+            item = in - head * a.items.d;
+            p = place_of<PAIRS>(a, item);
+            raw.load(static_cast<const S *>(a.src[0]) + (int64_t)(t0 + sub) * a.src_stride[0] + head * a.dim, p.lo, p.hi);
+        }
+        if (!formed) {
+            for (int e = threadIdx.x; e < tokens * a.half; e += kThreads) {
+                const int k = a.q_tokens == 1 ? 0 : e / a.half;
+                turns[e] = turn_at(a, t0 + k, e - k * a.half);
+            }
+            __syncthreads();
+            formed = true;
+        }
+        if (!live)
+            return;
+        float x[16];
+        raw.widen(x);
+        float2 turn[8];
+        if (8 * item < a.half) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                turn[e] = turns[sub * a.half + min(8 * item + e, a.half - 1)];
+            turn16<PAIRS>(a, item, turn, x);
+        }
+        store16(a, static_cast<uint16_t *>(a.q_out) + ((int64_t)(t0 + sub) * a.q_heads + head) * a.dim, p, x);
+    }
+}
 
+__device__ __forceinline__ uint32_t largest_of(const float *x, uint32_t top)
+{
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        top = max(top, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
+    return top;
+}
+
+__device__ __forceinline__ void put16(const Append8Args &a, uint8_t *out, Place p, const float *x, float inv)
+{
+    *reinterpret_cast<u32x2 *>(out + p.lo) = u32x2{codes4(a.e4m3, x, inv), codes4(a.e4m3, x + 4, inv)};
+    *reinterpret_cast<u32x2 *>(out + p.hi) = u32x2{codes4(a.e4m3, x + 8, inv), codes4(a.e4m3, x + 12, inv)};
+}
+
+// One token: a wave takes as many rows as it has lanes for.  items is a power of two.
+template <class S, bool PAIRS>
+__device__ __forceinline__ void write_token(const Append8Args &a, const Run &r, int row, int end, int item)
+{
+    const bool live = row < end;
+    const int v = live && row >= a.heads, head = v ? row - a.heads : row;
+    const Place p = v ? Place{16 * item, 16 * item + 8} : place_of<PAIRS>(a, item);
+    Raw16<S> raw;
+    Target to{};
+    int old = 0;
+    float2 turn[8];
+    if (live) {
+        raw.load(static_cast<const S *>(v ? a.src[2] : a.src[1]) + (int64_t)r.first * (v ? a.src_stride[2] : a.src_stride[1]) + head * a.dim,
+                 p.lo, p.hi);
+        to = target_of(a, r.block, v, head);
+        if (!r.begun)
+            old = *to.scale;
+    }
+    turns_of(a, r.first, item, turn);
+    float x[16];
+    uint32_t top = 0;
+    if (live) {
+        raw.widen(x);
+        if (!v)
+            turn16<PAIRS>(a, item, turn, x);
+        top = largest_of(x, 0);
+    }
+    for (int d = 1; d < (int)a.items.d; d *= 2)
+        top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if (!live)
+        return;
+    const int b = r.begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
+    if (!r.begun && b > old && b < 255)
+        rescale(a, r, to, old, b, item, a.items.d);
+    if (item == 0)
+        *to.scale = (uint8_t)b;
+    put16(a, to.codes + (r.slot - r.block * (int)a.block.d) * to.place, p, x, inverse_of(b));
+}
+
+// The wide path: 16-byte vectors of whole rows.  PP: tokens that a lane holds values of;
+// TEAM: waves that hold a run's head together.  A run of more tokens than that (two of one
+// slot are in it) is taken in parts.
+template <class S, bool PAIRS, int PP, int TEAM>
+__global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
+{
+    extern __shared__ float2 turns[];
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (group_here() >= a.groups)
         return;
-    if (group_here() >= a.kv_groups) { // q
-        const int group = group_here() - a.kv_groups, at = div_by(a.q_shares, group), share = group - at * a.q_shares.d;
-        const uint32_t t = ((uint32_t)at * kWaves + wave) * per + sub;
-        if (sub >= per || t >= (uint32_t)a.tokens)
-            return;
-        const int h1 = min((share + 1) * a.q_share, a.q_heads);
-        float2 turn[8];
-        turns_of(a, t, item, turn);
-        const S *row = static_cast<const S *>(a.src[0]) + (int64_t)t * a.src_stride[0];
-        uint16_t *out = static_cast<uint16_t *>(a.q_out) + (int64_t)t * a.q_heads * a.dim;
-        for (int h = share * a.q_share; h < h1; ++h) {
-            float x[16];
-            load16(row + h * a.dim, kq.lo, kq.hi, x);
-            turn16(a, item, turn, x);
-            store16(a, out + h * a.dim, kq, x);
-        }
+    if (group_here() >= a.kv_groups) {
+        turn_q<S, PAIRS>(a, group_here() - a.kv_groups, turns);
         return;
     }
-
+    const int sub = div_by(a.items, lane), item = lane - sub * a.items.d;
+    const int per = kWave / (int)a.items.d; // tokens of a wave at a time
+    const Place kq = place_of<PAIRS>(a, item), plain{16 * item, 16 * item + 8};
+    const int me = TEAM == 1 ? 0 : wave;
     __shared__ uint32_t largest[2][kWaves];
     int turned = 0; // which half of `largest`
-    each_run(a, group_here(), [&](Run r, int share) {
-        const int most = kWaves * PP * per;
+    int dealt = 0;  // pieces of work given to waves so far
+    each_run(a, group_here(), [&](const Run &r, int share) {
+        const int row0 = share * a.kv_share, end = min(row0 + a.kv_share, 2 * a.heads);
+        if (r.n == 1 && (a.items.d & (a.items.d - 1)) == 0) {
+            const int pieces = (end - row0 + per - 1) / per;
+            for (int i = (wave - dealt) & (kWaves - 1); i < pieces; i += kWaves)
+                write_token<S, PAIRS>(a, r, row0 + i * per + sub, end, item);
+            dealt += pieces;
+            return;
+        }
+        const int most = TEAM * PP * per;
         for (int left = r.n; left > 0; left -= most) {
             const int from = r.first + (r.n - left), n = min(left, most);
-            // waves of a team, which takes a head together
-            const int passes = (n + per - 1) / per, team = passes == 1 ? 1 : passes == 2 ? 2 : 4, me = wave & (team - 1);
+            const bool begun = r.begun && from == r.first;
             uint32_t t[PP];
+            int place[PP];
             bool live[PP];
-            float2 turn[PP][8];
-            bool formed = false;
 #pragma unroll
             for (int i = 0; i < PP; ++i) {
-                const int off = (i * team + me) * per + sub;
+                const int off = (i * TEAM + me) * per + sub;
                 t[i] = (uint32_t)from + off;
                 live[i] = sub < per && off < n;
+                place[i] = live[i] ? a.slots[t[i]] - r.block * (int)a.block.d : 0;
             }
-            const int last = min((share + 1) * a.kv_share, 2 * a.heads);
-            for (int row0 = share * a.kv_share; row0 < last; row0 += kWaves / team) {
-                const int row = row0 + wave / team;
-                const bool on = row < last;
+            float2 turn[PP][8];
+            Raw16<S> raw[PP];
+            const auto load = [&](int row) {
                 const int v = row >= a.heads, head = v ? row - a.heads : row;
                 const Place p = v ? plain : kq;
+                const S *src = static_cast<const S *>(v ? a.src[2] : a.src[1]) + head * a.dim;
+                const int64_t stride = v ? a.src_stride[2] : a.src_stride[1];
+#pragma unroll
+                for (int i = 0; i < PP; ++i)
+                    if (live[i])
+                        raw[i].load(src + (int64_t)t[i] * stride, p.lo, p.hi);
+            };
+            const int step = kWaves / TEAM;
+            int row = row0 + (TEAM == 1 ? (wave - dealt) & (kWaves - 1) : 0);
+            dealt += TEAM == 1 ? end - row0 : 0;
+            if (row < end)
+                load(row);
+#pragma unroll
+            for (int i = 0; i < PP; ++i)
+                if (row < a.heads && live[i]) // a first row of v: so are the others
+                    turns_of(a, t[i], item, turn[i]);
+            for (; row < end; row += step) {
+                const int v = row >= a.heads, head = v ? row - a.heads : row;
+                const Place p = v ? plain : kq;
+                const Target to = target_of(a, r.block, v, head);
+                int old = 0;
+                if (!begun)
+                    old = *to.scale;
                 float x[PP][16];
                 uint32_t top = 0;
-                Target to{};
-                int old = 0;
-                if (on) {
-                    to = target_of(a, r.block, v, head);
-                    if (!r.begun || from != r.first)
-                        old = *to.scale;
 #pragma unroll
-                    for (int i = 0; i < PP; ++i)
-                        if (live[i])
-                            load16(static_cast<const S *>(a.src[1 + v]) + (int64_t)t[i] * a.src_stride[1 + v] + head * a.dim, p.lo, p.hi,
-                                   x[i]);
-                    if (!v && !formed) {
-#pragma unroll
-                        for (int i = 0; i < PP; ++i)
-                            if (live[i])
-                                turns_of(a, t[i], item, turn[i]);
-                        formed = true;
+                for (int i = 0; i < PP; ++i)
+                    if (live[i]) {
+                        raw[i].widen(x[i]);
+                        if (!v)
+                            turn16<PAIRS>(a, item, turn[i], x[i]);
+                        top = largest_of(x[i], top);
                     }
-#pragma unroll
-                    for (int i = 0; i < PP; ++i)
-                        if (live[i]) {
-                            if (!v)
-                                turn16(a, item, turn[i], x[i]);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                top = max(top, __builtin_bit_cast(uint32_t, x[i][e]) & 0x7fffffffu);
-                        }
-                    top = wave_max(top);
-                }
-                if (team > 1) {
+                if (row + step < end)
+                    load(row + step); // on its way while this one is written
+                top = wave_max(top);
+                if constexpr (TEAM > 1) {
                     if (lane == 0)
                         largest[turned][wave] = top;
                     __syncthreads();
-                    for (int w = 0; w < team; ++w)
-                        top = max(top, largest[turned][wave - me + w]);
+                    for (int w = 0; w < TEAM; ++w)
+                        top = max(top, largest[turned][w]);
                     turned ^= 1; // the next head's go where none reads any more
                 }
-                if (!on)
-                    continue;
-                const bool begun = r.begun && from == r.first;
                 const int b = begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
                 if (!begun && b > old && b < 255)
-                    rescale(a, r, to, old, b, me * kWave + lane, team * kWave);
+                    rescale(a, r, to, old, b, me * kWave + lane, TEAM * kWave);
                 const float inv = inverse_of(b);
                 if (me == 0 && lane == 0)
                     *to.scale = (uint8_t)b;
 #pragma unroll
                 for (int i = 0; i < PP; ++i)
-                    if (live[i]) {
-                        uint8_t *out = to.codes + (a.slots[t[i]] - r.block * (int)a.block.d) * to.place;
-                        *reinterpret_cast<u32x2 *>(out + p.lo) = u32x2{codes4(a.e4m3, x[i], inv), codes4(a.e4m3, x[i] + 4, inv)};
-                        *reinterpret_cast<u32x2 *>(out + p.hi) =
-                            u32x2{codes4(a.e4m3, x[i] + 8, inv), codes4(a.e4m3, x[i] + 12, inv)};
-                    }
+                    if (live[i])
+                        put16(a, to.codes + place[i] * to.place, p, x[i], inv);
             }
-            __syncthreads(); // a further part's and a further run's reads of this one's writes; `largest`
+            if (left > most)
+                __syncthreads(); // the further part's reads of this one's writes
         }
     });
 }
@@ -399,11 +504,11 @@ template <class S> __global__ __launch_bounds__(kThreads) void paged8_append_gen
     };
     if (group_here() >= a.groups)
         return;
-    if (group_here() >= a.kv_groups) { // q: a workgroup for a token's share of heads
+    if (group_here() >= a.kv_groups) { // q: a workgroup for a share of a token's values
         const int group = group_here() - a.kv_groups, t = div_by(a.q_shares, group), share = group - t * a.q_shares.d;
-        const int h0 = share * a.q_share, h1 = min(h0 + a.q_share, a.q_heads);
+        const int e0 = share * a.q_share * 16, e1 = min(e0 + a.q_share * 16, a.q_heads * a.dim);
         uint16_t *out = static_cast<uint16_t *>(a.q_out) + (int64_t)t * a.q_heads * a.dim;
-        for (int i = h0 * a.dim + threadIdx.x; i < h1 * a.dim; i += kThreads) {
+        for (int i = e0 + threadIdx.x; i < e1; i += kThreads) {
             const int h = i / a.dim;
             const float x = value(0, t, h, i - h * a.dim);
             out[i] = (uint16_t)(a.bf ? pack2<true>(x, 0.0f) : pack2<false>(x, 0.0f));
@@ -444,12 +549,21 @@ template <class S> __global__ __launch_bounds__(kThreads) void paged8_append_gen
     });
 }
 
-template <class S> const void *kernel_of(int passes)
+// passes: tokens that a lane has to hold for a whole block, 0 for what the wide path does not take.
+template <class S, bool PAIRS> const void *kernel_of(int passes)
 {
-    return passes == 1   ? reinterpret_cast<const void *>(&paged8_append_kernel<S, 1>)
-           : passes == 2 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, 2>)
-           : passes == 4 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, 4>)
-                         : reinterpret_cast<const void *>(&paged8_append_generic_kernel<S>);
+    return passes <= 1   ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 1, 1>)
+           : passes <= 2 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 2, 1>)
+           : passes <= 4 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 4, 1>)
+           : passes <= 8 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 2, 4>)
+                         : reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 4, 4>);
+}
+
+template <class S> const void *kernel_of(bool pairs, int passes)
+{
+    return passes == 0 ? reinterpret_cast<const void *>(&paged8_append_generic_kernel<S>)
+           : pairs     ? kernel_of<S, true>(passes)
+                       : kernel_of<S, false>(passes);
 }
 
 } // namespace
@@ -491,41 +605,48 @@ extern "C" int gemv_paged8_append(const void *q, const void *k, const void *v, i
         wide = wide && reinterpret_cast<uintptr_t>(a.src[i]) % 16 == 0 && a.src_stride[i] * size % 16 == 0;
     const int items = cache->dim / 16, per = gemv::kWave / items; // lanes of a token's head, tokens of a wave at a time
     a.items = gemv::fast_div(items);
-    const int64_t need = (cache->block + gemv::kWaves * per - 1) / (gemv::kWaves * per); // passes of a whole block
-    const int passes = !wide || need > 4 ? 0 : need > 2 ? 4 : (int)need;
+    int64_t passes = (cache->block + per - 1) / per; // tokens that a lane holds of a whole block
+    if (!wide || passes > 16)
+        passes = 0;
 
-    // Enough workgroups to fill the card: rows of k and v are shared out four at a time,
-    // and from some 8000 workgroups on each looks for runs in more tokens instead.
+    // Enough workgroups to fill the card: all rows of a stretch of tokens to a workgroup
+    // where that gives some hundred, four rows (one a wave) where it does not.
     const int64_t rows = 2 * (int64_t)a.heads;
-    int64_t kv_share = 4, kv_shares = (rows + kv_share - 1) / kv_share;
-    int64_t stretch = (tokens * kv_shares + 8191) / 8192;
-    const int64_t most = cache->block < 32 ? cache->block : 32;
-    stretch = stretch < most ? stretch : most;
+    int64_t stretch = tokens / 1024;
+    stretch = stretch < 1 ? 1 : stretch < 16 ? stretch : 16;
     const int64_t stretches = (tokens + stretch - 1) / stretch;
+    int64_t kv_share = stretches >= 512 ? rows : 4;
+    kv_share = kv_share < 64 ? kv_share : 64;
+    int64_t kv_shares = (rows + kv_share - 1) / kv_share;
     while (stretches * kv_shares > gemv::kMostGroups && kv_share < rows) {
         kv_share *= 2;
         kv_shares = (rows + kv_share - 1) / kv_share;
     }
     a.stretch = (int)stretch, a.kv_share = (int)kv_share;
     const int64_t kv_groups = stretches * kv_shares;
-    const int64_t together = passes ? gemv::kWaves * per : 1; // tokens of a q workgroup
-    const int64_t q_groups = (tokens + together - 1) / together;
-    int64_t q_share = q_groups * q_heads / 4096;
-    q_share = q_share < 1 ? 1 : q_share < 8 ? q_share : 8;
-    while (q_groups * ((q_heads + q_share - 1) / q_share) > gemv::kMostGroups && q_share < q_heads)
+    // q: an item a thread; of heads so few that a token has fewer items, several tokens
+    const int64_t q_items = q_heads * items;
+    int64_t q_tokens = passes ? gemv::kThreads / q_items : 1;
+    const int64_t room = 1024 / (a.half > 0 ? a.half : 1); // turns that lie in LDS
+    q_tokens = q_tokens < room ? q_tokens : room;
+    q_tokens = q_tokens < 1 ? 1 : q_tokens;
+    const int64_t q_groups = (tokens + q_tokens - 1) / q_tokens;
+    int64_t q_share = tokens < 512 ? gemv::kThreads : 4 * gemv::kThreads;
+    q_share = q_share < q_items ? q_share : q_items;
+    while (q_groups * ((q_items + q_share - 1) / q_share) > gemv::kMostGroups && q_share < q_items)
         q_share *= 2;
-    const int64_t q_shares = (q_heads + q_share - 1) / q_share, groups = kv_groups + q_groups * q_shares;
+    const int64_t q_shares = (q_items + q_share - 1) / q_share, groups = kv_groups + q_groups * q_shares;
     if (groups > INT_MAX) // rows of a stride of 0 for more tokens and heads than any memory holds
         return GEMV_E_DIM;
-    a.q_share = (int)q_share;
+    a.q_share = (int)q_share, a.q_tokens = (int)q_tokens, a.q_items = gemv::fast_div(q_items);
     a.q_shares = gemv::fast_div(q_shares), a.kv_shares = gemv::fast_div(kv_shares);
     a.kv_groups = (int)kv_groups, a.groups = (int)groups;
-    const void *fn = src_type == GEMV_W_F32   ? gemv::kernel_of<float>(passes)
-                     : src_type == GEMV_W_F16 ? gemv::kernel_of<_Float16>(passes)
-                                              : gemv::kernel_of<__bf16>(passes);
+    const void *fn = src_type == GEMV_W_F32   ? gemv::kernel_of<float>(a.pairs, (int)passes)
+                     : src_type == GEMV_W_F16 ? gemv::kernel_of<_Float16>(a.pairs, (int)passes)
+                                              : gemv::kernel_of<__bf16>(a.pairs, (int)passes);
     void *args[] = {&a};
     const int64_t x = groups < gemv::kGroupsX ? groups : gemv::kGroupsX;
-    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)x, (unsigned)((groups + x - 1) / x)), dim3(gemv::kThreads), args, 0,
-                                         static_cast<hipStream_t>(hip_stream));
+    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)x, (unsigned)((groups + x - 1) / x)), dim3(gemv::kThreads), args,
+                                         (size_t)q_tokens * a.half * sizeof(float2), static_cast<hipStream_t>(hip_stream));
     return gemv::finish_launch((int)e);
 }
