@@ -396,17 +396,17 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
     const int sub = div_by(a.items, lane), item = lane - sub * a.items.d;
     const int per = kWave / (int)a.items.d; // tokens of a wave at a time
     const Place kq = place_of<PAIRS>(a, item), plain{16 * item, 16 * item + 8};
-    const int me = TEAM == 1 ? 0 : wave;
+    const int team = wave / TEAM, me = wave % TEAM;
     __shared__ uint32_t largest[2][kWaves];
     int turned = 0; // which half of `largest`
-    int dealt = 0;  // pieces of work given to waves so far
+    int dealt = 0, dealt_tokens = 0; // rows given to teams, and pieces of single tokens' rows to waves, so far
     each_run(a, group_here(), [&](const Run &r, int share) {
         const int row0 = share * a.kv_share, end = min(row0 + a.kv_share, 2 * a.heads);
         if (r.n == 1 && (a.items.d & (a.items.d - 1)) == 0) {
             const int pieces = (end - row0 + per - 1) / per;
-            for (int i = (wave - dealt) & (kWaves - 1); i < pieces; i += kWaves)
+            for (int i = (wave - dealt_tokens) & (kWaves - 1); i < pieces; i += kWaves)
                 write_token<S, PAIRS>(a, r, row0 + i * per + sub, end, item);
-            dealt += pieces;
+            dealt_tokens += pieces;
             return;
         }
         const int most = TEAM * PP * per;
@@ -435,19 +435,22 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
                     if (live[i])
                         raw[i].load(src + (int64_t)t[i] * stride, p.lo, p.hi);
             };
-            const int step = kWaves / TEAM;
-            int row = row0 + (TEAM == 1 ? (wave - dealt) & (kWaves - 1) : 0);
-            dealt += TEAM == 1 ? end - row0 : 0;
+            constexpr int kTeams = kWaves / TEAM;
+            int row = row0 + ((team - dealt) & (kTeams - 1));
+            if constexpr (TEAM == 1)
+                dealt += end - row0;
             if (row < end)
                 load(row);
 #pragma unroll
             for (int i = 0; i < PP; ++i)
                 if (row < a.heads && live[i]) // a first row of v: so are the others
                     turns_of(a, t[i], item, turn[i]);
-            for (; row < end; row += step) {
+            // teams of several waves go through as many rounds each: they meet in every one
+            for (int left_rows = end - row0; TEAM == 1 ? row < end : left_rows > 0; row += kTeams, left_rows -= kTeams) {
+                const bool on = row < end;
                 const int v = row >= a.heads, head = v ? row - a.heads : row;
                 const Place p = v ? plain : kq;
-                const Target to = target_of(a, r.block, v, head);
+                const Target to = target_of(a, r.block, v, on ? head : 0);
                 int old = 0;
                 if (!begun)
                     old = *to.scale;
@@ -461,16 +464,19 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
                             turn16<PAIRS>(a, item, turn[i], x[i]);
                         top = largest_of(x[i], top);
                     }
-                if (row + step < end)
-                    load(row + step); // on its way while this one is written
+                if (row + kTeams < end)
+                    load(row + kTeams); // on its way while this one is written
                 top = wave_max(top);
                 if constexpr (TEAM > 1) {
                     if (lane == 0)
                         largest[turned][wave] = top;
                     __syncthreads();
+#pragma unroll
                     for (int w = 0; w < TEAM; ++w)
-                        top = max(top, largest[turned][w]);
+                        top = max(top, largest[turned][team * TEAM + w]);
                     turned ^= 1; // the next head's go where none reads any more
+                    if (!on)
+                        continue;
                 }
                 const int b = begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
                 if (!begun && b > old && b < 255)
@@ -553,8 +559,8 @@ template <class S> __global__ __launch_bounds__(kThreads) void paged8_append_gen
 template <class S, bool PAIRS> const void *kernel_of(int passes)
 {
     return passes <= 1   ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 1, 1>)
-           : passes <= 2 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 2, 1>)
-           : passes <= 4 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 4, 1>)
+           : passes <= 2 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 1, 2>)
+           : passes <= 4 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 1, 4>)
            : passes <= 8 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 2, 4>)
                          : reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 4, 4>);
 }
