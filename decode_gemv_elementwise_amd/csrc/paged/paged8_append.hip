@@ -41,6 +41,7 @@ struct Append8Args {
     FastDiv q_items;             // items of 16 values that a token's q has
     FastDiv q_shares, kv_shares; // workgroups that share one token's q, one stretch's k and v
     int32_t stretch;             // tokens in which a workgroup looks for runs
+    int32_t die_stretches;       // stretches of a die
     int32_t q_share, kv_share;   // items of q, rows of k and v of a workgroup
     int32_t q_tokens;            // tokens of a q workgroup
     int32_t kv_groups, groups;   // workgroups for k and v, and all
@@ -264,8 +265,12 @@ __device__ __forceinline__ int group_here() { return blockIdx.y * kGroupsX + blo
 template <class F> __device__ __forceinline__ void each_run(const Append8Args &a, int group, F one)
 {
     const int lane = threadIdx.x & (kWave - 1);
-    const int at = div_by(a.kv_shares, group), share = group - at * a.kv_shares.d;
-    const uint32_t t0 = (uint32_t)at * a.stretch;
+    // Workgroups go to the 8 dies in turn, and of a chunk's stretches one in so many begins a
+    // run: a die takes neighbouring ones, so that no die gets all of those.
+    const int turn = group / 8, at = div_by(a.kv_shares, turn), share = turn - at * a.kv_shares.d;
+    const uint32_t t0 = ((uint32_t)(group % 8) * a.die_stretches + at) * a.stretch;
+    if (t0 >= (uint32_t)a.tokens)
+        return;
     // lane i: does a run begin at token t0 + i; a stretch is shorter than a wave
     const int slot = slot_at(a, t0 + lane), before = slot_at(a, t0 + lane - 1), mine = block_of(a, slot);
     uint64_t begins = __ballot(lane < a.stretch && mine >= 0 && mine != block_of(a, before));
@@ -324,6 +329,15 @@ template <class S, bool PAIRS> __device__ __forceinline__ void turn_q(const Appe
         }
         store16(a, static_cast<uint16_t *>(a.q_out) + ((int64_t)(t0 + sub) * a.q_heads + head) * a.dim, p, x);
     }
+}
+
+// A barrier for what lies in LDS: __syncthreads would wait for every store to memory on
+// its way, some us a head.
+__device__ __forceinline__ void meet()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 __device__ __forceinline__ uint32_t largest_of(const float *x, uint32_t top)
@@ -470,7 +484,8 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
                 if constexpr (TEAM > 1) {
                     if (lane == 0)
                         largest[turned][wave] = top;
-                    __syncthreads();
+                    asm volatile("" ::"v"(old)); // read by all before one of them writes the new one
+                    meet();
 #pragma unroll
                     for (int w = 0; w < TEAM; ++w)
                         top = max(top, largest[turned][team * TEAM + w]);
@@ -615,14 +630,18 @@ extern "C" int gemv_paged8_append(const void *q, const void *k, const void *v, i
     if (!wide || passes > 16)
         passes = 0;
 
-    // Enough workgroups to fill the card: all rows of a stretch of tokens to a workgroup
-    // where that gives some hundred, four rows (one a wave) where it does not.
+    // Some thousand workgroups for k and v, each for four rows (one a wave) of a stretch of
+    // tokens: of a chunk few begin a run, and more rows would be taken one after the other
+    // (8192 tokens, blocks of 64: 38 us with 4 rows, 43 with 8, 52 with 16; 512 tokens 10,
+    // 15, 15).  Where the tokens are many and a wave or two hold a block's, eight: fewer
+    // workgroups form the same angles, and single tokens' rows fill a wave (8192 tokens in
+    // blocks of 16 40 us, 44 with 4 rows; 4096 single tokens 24 and 34).
     const int64_t rows = 2 * (int64_t)a.heads;
-    int64_t stretch = tokens / 1024;
-    stretch = stretch < 1 ? 1 : stretch < 16 ? stretch : 16;
-    const int64_t stretches = (tokens + stretch - 1) / stretch;
-    int64_t kv_share = stretches >= 512 ? rows : 4;
-    kv_share = kv_share < 64 ? kv_share : 64;
+    int64_t kv_share = tokens >= 2048 && passes <= 2 ? 8 : 4;
+    int64_t stretch = tokens * ((rows + kv_share - 1) / kv_share) / 1024;
+    stretch = stretch < 1 ? 1 : stretch < 32 ? stretch : 32;
+    const int64_t per_die = ((tokens + stretch - 1) / stretch + 7) / 8, stretches = 8 * per_die;
+    a.die_stretches = (int)per_die;
     int64_t kv_shares = (rows + kv_share - 1) / kv_share;
     while (stretches * kv_shares > gemv::kMostGroups && kv_share < rows) {
         kv_share *= 2;
