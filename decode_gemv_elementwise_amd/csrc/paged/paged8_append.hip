@@ -248,7 +248,7 @@ __device__ __forceinline__ void rescale(const Append8Args &a, const Run &r, cons
         u32x4 x = *w;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const f32x4 y = a.e4m3 ? floats4<GEMV_KV_E4M3>(x[e], 1.0f) : floats4<GEMV_KV_INT8>(x[e], 1.0f);
+            const f32x4 y = a.e4m3 ? floats4<GEMV_KV_E4M3>(x[e]) : floats4<GEMV_KV_INT8>(x[e]);
             const float z[4] = {y[0], y[1], y[2], y[3]};
             x[e] = codes4(a.e4m3, z, f);
         }

@@ -70,6 +70,16 @@ extern "C" int gemv_paged8_attn(const void *q, int q_type, int64_t q_token_strid
     const void *fn = cache->dim == 64    ? gemv::paged8_attn_kernel_64(cache->code, bf, f32out, runs, many)
                      : cache->dim == 128 ? gemv::paged8_attn_kernel_128(cache->code, bf, f32out, runs, many)
                                          : gemv::paged8_attn_kernel_256(cache->code, bf, f32out, runs, many);
+    // Where a token's heads lie one after the other in memory, rows of 128 bytes and less
+    // are read by tiles of several of them: 64 single tokens over up to 16384 keys each,
+    // 8 heads of 128 in e4m3, 203 us by four heads, 214 by two and 226 by one (196 where a
+    // page's rows of one head lie together); of 64 130, 133 and 180; of 256 280, 266 and 265.
+    // Tiles enough have to be left, or one is cut into so many parts that joining them takes
+    // longest: one request of 131072 keys 106 us by four heads, 72 by one.
+    const bool apart = cache->k_stride[2] >= cache->k_stride[1] || cache->v_stride[2] >= cache->v_stride[1];
+    a.spread = many || apart || cache->dim > 128 ? 0 : a.heads % 4 == 0 ? 2 : a.heads % 2 == 0 ? 1 : 0;
+    while (a.spread > 0 && requests * a.heads >> a.spread < 128)
+        --a.spread;
     // no more workgroups than shares can be: row tiles times the blocks that the
     // table's width allows
     const int64_t blocks = (a.reach + gemv::kCostBlock - 1) / gemv::kCostBlock;

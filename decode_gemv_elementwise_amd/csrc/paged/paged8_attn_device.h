@@ -17,11 +17,13 @@ namespace {
 
 constexpr uint32_t kMostCost = INT_MAX;
 constexpr int kCostBlock = 32; // keys of a block, as the plan counts
+constexpr uint32_t kSpreadFrom = 64; // such blocks of a workgroup, from which on tiles are of several heads
 
 struct Attn8Args : AttnArgs { // k and v are bytes
     const uint8_t *k_scale, *v_scale;
     uint32_t ks_stride[3], vs_stride[3]; // page, block in page, head; below 2^31
     FastDiv block;
+    int32_t spread; // a tile of few rows may be of 2^spread heads, a divisor of all: 1, 2 or 4
 };
 
 // The kernel's arguments, read again from here on.
@@ -114,6 +116,7 @@ template <class TILE> __device__ __forceinline__ void run_plan(char *lds)
         __syncthreads();
     }
 
+    int spread = 0, stride = TILE::kPart; // floats from one part's place to the next
     // this workgroup's share [x, x1): every group has `each` places, the first `more` one in addition
     uint32_t base = 0, x = 0, x1 = 0, each = 0, more = 0, edge = 0;
     // Neighbouring shares go to one of the 8 dies, which share an L2 cache; and where a
@@ -137,28 +140,36 @@ template <class TILE> __device__ __forceinline__ void run_plan(char *lds)
         if (r0 == 0) {
             if (once)
                 total = here;
+            if (total == kMostCost)
+                return;
+            if (total >= gridDim.x * kSpreadFrom) {
+                spread = a.spread;
+                stride <<= spread;
+                total >>= spread; // nothing is lost: every tile was counted once for each head
+            }
             const uint32_t groups = uniform(min(gridDim.x, (total + TILE::kLeast - 1) / TILE::kLeast));
-            if (w >= groups || total == kMostCost)
+            if (w >= groups)
                 return;
             each = uniform(total / groups);
             more = total - each * groups;
             x = w * each + min(w, more);
             x1 = x + each + (w < more);
             // a tile is cut only if the parts have room: two for each workgroup, below 2^28 floats in all
-            edge = a.part_room < 2 * (int64_t)groups * TILE::kPart ? kMostCost / 2 : TILE::kEdge;
+            edge = a.part_room < 2 * (int64_t)groups * stride ? kMostCost / 2 : TILE::kEdge;
         }
+        here >>= spread;
         while (x < x1 && x < base + here) {
             int lo = 0, hi = min(kThreads, a.requests - r0);
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (before[mid] <= x - base)
+                if (before[mid] >> spread <= x - base)
                     lo = mid;
                 else
                     hi = mid;
             }
             lo = uniform(lo);
             const Request q = {(int)uniform(requests[lo].q0), (int)uniform(requests[lo].n), (int)uniform(requests[lo].kv)};
-            const uint32_t y = x - base - uniform(before[lo]), nb = uniform(cost_of(q)), tiles = uniform(tiles_of(q));
+            const uint32_t y = x - base - (uniform(before[lo]) >> spread), nb = uniform(cost_of(q)), tiles = uniform(tiles_of(q));
             const uint32_t unit = uniform(y / nb), start = x - (y - unit * nb); // of the tile
             // both ends of the share, as places of this tile; one near an edge of it moves there
             const auto moved = [&](uint32_t b) {
@@ -168,7 +179,7 @@ template <class TILE> __device__ __forceinline__ void run_plan(char *lds)
             x = start + nb;
             if (b0 >= b1)
                 continue;
-            Share sh{(int)b0, (int)(b1 - b0), (int)nb, 1, 0, 0, TILE::kPart};
+            Share sh{(int)b0, (int)(b1 - b0), (int)nb, 1, 0, 0, stride};
             if (sh.len < (int)nb) {
                 const auto group_of = [&](uint32_t place) {
                     const uint32_t longer = more * (each + 1);
@@ -179,7 +190,7 @@ template <class TILE> __device__ __forceinline__ void run_plan(char *lds)
                 sh.me = w - sh.first;
             }
             const int head = uniform(unit / tiles), tile = unit - head * tiles;
-            TILE::run(arguments(), q, r0 + lo, tile, head, sh, lds);
+            TILE::run(arguments(), q, r0 + lo, tile, head << spread, 1 << spread, sh, lds);
         }
         if (x >= x1)
             return;

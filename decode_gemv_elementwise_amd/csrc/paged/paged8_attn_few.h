@@ -48,6 +48,7 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
     u32x4 qf[KS];
     f32x4 o[VPL];
     float m, l, scale;
+    int window, sinks; // of the arguments, kept: read again at every block they would be waited for
     uint32_t special; // not 0: an infinity or NaN of v was taken out
 
     __device__ FewRows(const Attn8Args &args) : a(args) {}
@@ -62,6 +63,7 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
         p_hi = before + (int)div_by(a.per_group, min(row0 + kRows, rows) - 1);
         at.begin(a, r, head);
         scale = kept(a.scale_log2);
+        window = kept(a.window), sinks = kept(a.sinks);
         p_row = -1;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
@@ -82,6 +84,16 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
             o[i] = f32x4{0, 0, 0, 0};
     }
 
+    __device__ __forceinline__ bool sees(int j) const
+    {
+        return j <= p_row && (window == 0 || j > p_row - window || j < sinks);
+    }
+    // Every row of the tile sees every key of [j0, j0 + n).
+    __device__ __forceinline__ bool sees_all(int j0, int n) const
+    {
+        return j0 + n - 1 <= p_lo && (window == 0 || j0 > p_hi - window || j0 + n <= sinks);
+    }
+
     // Page ids of a block's keys that this lane reads, as the table has them (they are
     // checked where they are used, so that their load is waited for there): of k the keys
     // krun and krun + 4, of v the eight from vrun on.
@@ -93,7 +105,8 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
         u32x4 k[2][KL];
         uint32_t v[8][VL];
         uint32_t has;
-        uint8_t ks[NK], vs[NV];
+        uint8_t ks[NV], vs[NV];
+        int vid[NV]; // checked pages of v's keys
     };
 
     __device__ __forceinline__ int krun(int j0) const { return j0 + 8 * (col >> 2) + (col & 3); }
@@ -109,20 +122,23 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
             ids.v[i] = at.raw(vrun(j0) + i);
     }
 
-    // Asks for a block's k and v.
-    __device__ __forceinline__ void load(int j0, const Ids &ids, Data &x) const
+    // Asks for a block's k and the scales of both.
+    __device__ __forceinline__ void load_k(int j0, const Ids &ids, Data &x) const
     {
-        int kid[NK], vid[NV];
+        int kid[NK];
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
+        for (int i = 0; i < NK; ++i)
             kid[i] = at.checked(ids.k[i]);
-            x.ks[i] = *at.template scale<false>(kid[i], krun(j0) + 4 * i);
-        }
+        x.has = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            vid[i] = at.checked(ids.v[i]);
-            x.vs[i] = *at.template scale<true>(vid[i], vrun(j0) + i);
+            x.vid[i] = at.checked(ids.v[i]);
+            x.ks[i] = *at.template scale<false>(x.vid[i], vrun(j0) + i);
+            x.vs[i] = *at.template scale<true>(x.vid[i], vrun(j0) + i);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x.has |= (uint32_t)(x.vid[RUNS ? 0 : i] >= 0) << i;
         const uint8_t *kp = at.template codes<false>(kid[0], krun(j0)) + 16 * grp;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -132,10 +148,15 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
             for (int s = 0; s < KL; ++s)
                 x.k[i][s] = *reinterpret_cast<const u32x4 *>(src + 64 * s);
         }
-        const uint8_t *vp = at.template codes<true>(vid[0], vrun(j0)) + VPL * col;
+    }
+
+    // Asks for its v.
+    __device__ __forceinline__ void load_v(int j0, Data &x) const
+    {
+        const uint8_t *vp = at.template codes<true>(x.vid[0], vrun(j0)) + VPL * col;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint8_t *src = RUNS ? vp + (uint64_t)i * at.v1 : at.template codes<true>(vid[RUNS ? 0 : i], vrun(j0) + i) + VPL * col;
+            const uint8_t *src = RUNS ? vp + (uint64_t)i * at.v1 : at.template codes<true>(x.vid[RUNS ? 0 : i], vrun(j0) + i) + VPL * col;
             if constexpr (VL == 1) {
                 x.v[i][0] = *reinterpret_cast<const uint32_t *>(src);
             } else if constexpr (VL == 2) {
@@ -149,10 +170,6 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
                     x.v[i][e] = y[e];
             }
         }
-        x.has = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x.has |= (uint32_t)(vid[RUNS ? 0 : i] >= 0) << i;
         __builtin_amdgcn_sched_barrier(0); // all are asked for before anything waits for one
     }
 
@@ -161,29 +178,38 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
         float p[8];
         {
             f32x4 s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
-            const float k0 = scale_of(x.ks[0]), k1 = scale_of(x.ks[NK - 1]);
+            const auto codes = [](u32x4 w, int s) {
+                const u32x2 x = codes16<CODE, BF>(w[s % 2 * 2]), y = codes16<CODE, BF>(w[s % 2 * 2 + 1]);
+                return u32x4{x[0], x[1], y[0], y[1]};
+            };
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                s0 = mfma16<BF>(widen8<CODE, BF>(x.k[0][s / 2][s % 2 * 2], x.k[0][s / 2][s % 2 * 2 + 1], k0), qf[s], s0);
-                s1 = mfma16<BF>(widen8<CODE, BF>(x.k[1][s / 2][s % 2 * 2], x.k[1][s / 2][s % 2 * 2 + 1], k1), qf[s], s1);
+                s0 = mfma16<BF>(codes(x.k[0][s / 2], s), qf[s], s0);
+                s1 = mfma16<BF>(codes(x.k[1][s / 2], s), qf[s], s1);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            // a lane's scores are of the keys vrun, whose scales of k are asked for with v's
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[i] = s0[i] * scale;
-                p[4 + i] = s1[i] * scale;
+                p[i] = s0[i] * (scale * scale_of(x.ks[RUNS ? 0 : i]));
+                p[4 + i] = s1[i] * (scale * scale_of(x.ks[RUNS ? 0 : 4 + i]));
             }
         }
         // every row of the tile sees every key of the block
-        const bool whole = sees_all(a, p_lo, p_hi, j0, kBlock) && !__any(x.has != 0xff);
+        const bool whole = sees_all(j0, kBlock) && !__any(x.has != 0xff);
+        uint32_t seen = 0xff; // this row sees the lane's i-th key
         if (!whole) {
+            seen = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                p[i] = (x.has >> i & 1) && sees(a, p_row, vrun(j0) + i) ? p[i] : kNegInf;
+            for (int i = 0; i < 8; ++i) {
+                const bool see = (x.has >> i & 1) && sees(vrun(j0) + i);
+                seen |= (uint32_t)see << i;
+                p[i] = see ? p[i] : kNegInf;
+            }
         }
         float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-        top = fmaxf(m, row_max(top));
-        if (__any(top > m)) {
+        if (__any(top > m)) { // else it moves in no lane, nor in those that share its row
+            top = fmaxf(m, row_max(top));
             const float f = top == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - top);
             l *= f;
 #pragma unroll
@@ -196,6 +222,10 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
         for (int i = 0; i < 8; ++i) {
             p[i] = __builtin_amdgcn_exp2f(BF ? p[i] - base : p[i] - base + kF16Lift);
             l += p[i];
+            // bf16 has the range to take v's scale on the weight, a power of two: the codes
+            // need no product then.  Of a NaN scale only rows that see the key take it.
+            if constexpr (BF)
+                p[i] = seen >> i & 1 ? p[i] * scale_of(x.vs[RUNS ? 0 : i]) : 0.0f;
         }
         u32x4 pf, pl; // the weights in 16 bits; the second piece of them
         if constexpr (F32OUT) {
@@ -218,7 +248,7 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
             uint32_t v[8][2];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const u32x2 y = widen4<CODE, BF>(x.v[i][w], scale_of(x.vs[RUNS ? 0 : i]));
+                const u32x2 y = BF ? codes16<CODE, BF>(x.v[i][w]) : widen4<CODE, BF>(x.v[i][w], Scale<CODE, BF>(x.vs[RUNS ? 0 : i]));
                 v[i][0] = y[0];
                 v[i][1] = y[1];
             }
@@ -261,10 +291,10 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
 #pragma unroll 1
         for (int j = j0; j < j0 + n; ++j) {
             const int id = at.checked(at.raw(j));
-            if (id < 0 || !sees(a, p_row, j))
+            if (id < 0 || !sees(j))
                 continue;
             const uint8_t *src = at.template codes<true>(id, j) + 4 * VPL * grp;
-            const float f = scale_of(*at.template scale<true>(id, j));
+            const Scale<CODE, BF> f(*at.template scale<true>(id, j));
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -281,76 +311,71 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
     }
 };
 
-// One share of a tile of few rows.  SUB: blocks of 32 keys that a wave takes in one
-// round; EVERY: what the plan counts at least for a share, in such blocks.
-template <int CODE, bool BF, int D, bool F32OUT, bool RUNS, int SUB> struct FewTile {
+// One share of a tile of few rows.  A wave has the next block's k and v on their way; of
+// the widest heads, for which there are no registers, its k, and asks for v at a block's
+// start.  A tile may be of `spread` neighbouring heads (1, 2 or 4), each with its
+// share of the four waves: where a token's heads lie together in memory the waves then
+// read neighbouring rows at one time.
+template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewTile {
     typedef FewRows<CODE, BF, D, F32OUT, RUNS> Rows;
     static constexpr int kRows = Rows::kRows, kPart = few_part(D);
     static constexpr uint32_t kLeast = D == 64 ? 16 : 8, kEdge = kLeast;
     static constexpr int kBuffer = kRows * (D + 4); // floats: a wave's sums, padded so that the lanes of a group meet no bank
 
-    // lds: kWaves buffers, free again on return
-    static __device__ __forceinline__ void run(const Attn8Args &a, const Request &rq, int r, int tile, int head,
+    // lds: kWaves buffers, free again on return.  head: the tile's first.
+    static __device__ __forceinline__ void run(const Attn8Args &a, const Request &rq, int r, int tile, int head, int spread,
                                                const Share &sh, char *lds)
     {
-        constexpr int VPL = D / 16, ROW = D + 4, kStep = SUB * Rows::kBlock;
+        constexpr int VPL = D / 16, ROW = D + 4;
         __shared__ float lds_m[kWaves * kRows], lds_l[kWaves * kRows];
         __shared__ int lds_last;
         float *const buffers = reinterpret_cast<float *>(lds);
         const int thread = thread_here(), wave = uniform(thread / kWave);
+        const int waves = kWaves / spread; // of a head
 
         Rows t(a);
-        t.begin(rq, r, tile, head, thread);
-        const Walk walk = walk_of<kStep>(a, t.p_lo, t.p_hi);
+        t.begin(rq, r, tile, head + wave / waves, thread);
+        const Walk walk = walk_of<Rows::kBlock>(a, t.p_lo, t.p_hi);
         // shares begin at whole rounds of the waves
-        const int b0 = sh.from(walk.count) & -kWaves;
-        const int b1 = sh.b + sh.len == sh.nb ? walk.count : sh.to(walk.count) & -kWaves;
-        const auto key = [&](int b) { return walk.block(b) * kStep; };
-        // A round's page ids are asked for two rounds ahead and its k and v one round ahead.
-        int b = b0 + wave;
-        typename Rows::Ids ids[SUB];
-        typename Rows::Data x[SUB], y[SUB];
-        const auto ask_ids = [&](int b) {
-#pragma unroll
-            for (int i = 0; i < SUB; ++i)
-                t.load_ids(key(b) + i * Rows::kBlock, ids[i]);
-        };
-        const auto ahead = [&](int b, typename Rows::Data *x) {
+        const int b0 = sh.from(walk.count) & -waves;
+        const int b1 = sh.b + sh.len == sh.nb ? walk.count : sh.to(walk.count) & -waves;
+        const auto key = [&](int b) { return walk.block(b) * Rows::kBlock; };
+        // A block's page ids are asked for two rounds ahead, its k and v one.
+        constexpr bool kLate = D == 256;
+        int b = b0 + (wave & (waves - 1));
+        typename Rows::Ids ids;
+        typename Rows::Data x, y;
+        const auto ahead = [&](int b, typename Rows::Data &x) {
             if (b < b1) {
-                typename Rows::Ids now[SUB];
-#pragma unroll
-                for (int i = 0; i < SUB; ++i)
-                    now[i] = ids[i];
-                if (b + kWaves < b1)
-                    ask_ids(b + kWaves);
-#pragma unroll
-                for (int i = 0; i < SUB; ++i)
-                    t.load(key(b) + i * Rows::kBlock, now[i], x[i]);
+                const typename Rows::Ids now = ids;
+                if (b + waves < b1)
+                    t.load_ids(key(b + waves), ids);
+                t.load_k(key(b), now, x);
+                if constexpr (!kLate)
+                    t.load_v(key(b), x);
             }
         };
-        const auto take = [&](int b, const typename Rows::Data *x) {
-#pragma unroll
-            for (int i = 0; i < SUB; ++i)
-                t.block(key(b) + i * Rows::kBlock, x[i]);
+        const auto round = [&](typename Rows::Data &x, typename Rows::Data &next) {
+            if constexpr (kLate)
+                t.load_v(key(b), x);
+            ahead(b + waves, next);
+            t.block(key(b), x);
+            b += waves;
         };
         if (b < b1)
-            ask_ids(b);
+            t.load_ids(key(b), ids);
         ahead(b, x);
         while (b < b1) {
-            ahead(b + kWaves, y);
-            take(b, x);
-            b += kWaves;
+            round(x, y);
             if (b >= b1)
                 break;
-            ahead(b + kWaves, x);
-            take(b, y);
-            b += kWaves;
+            round(y, x);
         }
         if (__any(t.special != 0))
-            for (b = b0 + wave; b < b1; b += kWaves)
-                t.add_special(key(b), kStep);
+            for (b = b0 + (wave & (waves - 1)); b < b1; b += waves)
+                t.add_special(key(b), Rows::kBlock);
 
-        // join the waves
+        // join the waves of a head
         const float l = row_sum(t.l);
         if (t.grp == 0) {
             lds_m[wave * kRows + t.col] = t.m;
@@ -359,8 +384,7 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS, int SUB> struct FewT
         __syncthreads();
         {
             float top = kNegInf;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w)
+            for (int w = wave & -waves; w < (wave & -waves) + waves; ++w)
                 top = fmaxf(top, lds_m[w * kRows + t.col]);
             const float f = t.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(t.m - top);
             float *dst = buffers + wave * kBuffer + t.col * ROW + 4 * VPL * t.grp;
@@ -371,138 +395,137 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS, int SUB> struct FewT
                     dst[e * VPL + c] = t.o[c][e] * f;
         }
         __syncthreads();
-        const int rows = min(rq.n * a.group - tile * kRows, kRows);
-        int row = thread / 16; // 16 threads to a row
-        const int d0 = (thread & 15) * VPL;
-        float top = kNegInf, sum = 0.0f, acc[VPL];
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            top = fmaxf(top, lds_m[w * kRows + row]);
-#pragma unroll
-        for (int c = 0; c < VPL; ++c)
-            acc[c] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float mw = lds_m[w * kRows + row];
-            sum += lds_l[w * kRows + row] * (mw == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mw - top)); // keeps a NaN
-#pragma unroll
-            for (int c = 0; c < VPL; ++c)
-                acc[c] += buffers[w * kBuffer + row * ROW + d0 + c];
-        }
-        bool write = row < rows;
-
-        if (sh.np > 1) {
-            if (write) {
-                const Parts parts(a);
-                const int mine = sh.part(sh.me);
-#pragma unroll
-                for (int c = 0; c < VPL; c += 4)
-                    parts.put4(mine + row * D + d0 + c, f32x4{acc[c], acc[c + 1], acc[c + 2], acc[c + 3]});
-                if (d0 == 0) {
-                    parts.put(mine + kRows * D + row, top);
-                    parts.put(mine + kRows * D + kRows + row, sum);
-                }
-            }
-            if (!last_part(a, sh, thread, &lds_last))
-                return;
-            // 16 threads to a row again; what rows the tile lacks gives the others more
-            // threads, each set of them taking every sets-th part
-            const int sets = kRows / rows, set = row / rows;
-            row -= set * rows;
-            top = kNegInf;
-            sum = 0.0f;
-#pragma unroll
-            for (int c = 0; c < VPL; ++c)
-                acc[c] = 0.0f;
-            if (set < sets) {
-                constexpr int kAhead = 4;
-                const Parts parts(a);
-                for (int i0 = set; i0 < sh.np; i0 += kAhead * sets) {
-                    float m[kAhead], s[kAhead];
-                    f32x4 x[kAhead][VPL / 4];
-#pragma unroll
-                    for (int u = 0; u < kAhead; ++u) {
-                        const int i = i0 + u * sets, at = sh.part(min(i, sh.np - 1));
-                        m[u] = parts.get(at + kRows * D + row);
-                        s[u] = parts.get(at + kRows * D + kRows + row);
-#pragma unroll
-                        for (int c = 0; c < VPL / 4; ++c)
-                            x[u][c] = parts.get4(at + row * D + d0 + 4 * c);
-                        if (i >= sh.np) {
-                            m[u] = kNegInf;
-                            s[u] = 0.0f;
-#pragma unroll
-                            for (int c = 0; c < VPL / 4; ++c)
-                                x[u][c] = f32x4{0, 0, 0, 0};
-                        }
-                    }
-                    float next = top;
-#pragma unroll
-                    for (int u = 0; u < kAhead; ++u)
-                        next = fmaxf(next, m[u]);
-                    const float f0 = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
-                    sum *= f0;
-#pragma unroll
-                    for (int c = 0; c < VPL; ++c)
-                        acc[c] *= f0;
-#pragma unroll
-                    for (int u = 0; u < kAhead; ++u) {
-                        const float f = m[u] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[u] - next);
-                        sum += s[u] * f;
-#pragma unroll
-                        for (int c = 0; c < VPL; ++c)
-                            acc[c] += x[u][c / 4][c % 4] * f;
-                    }
-                    top = next;
-                }
-            }
-            // join the sets: set 0 adds the others' in order.  They lie in the first
-            // buffer: at most 16 rows of VPL 16 floats, and their maxima and sums.
-            if (set < sets && set > 0) {
-                float *dst = buffers + (set * rows + row) * D + d0;
-#pragma unroll
-                for (int c = 0; c < VPL; c += 4)
-                    *reinterpret_cast<f32x4 *>(dst + c) = f32x4{acc[c], acc[c + 1], acc[c + 2], acc[c + 3]};
-                if (d0 == 0) {
-                    lds_m[set * rows + row] = top;
-                    lds_l[set * rows + row] = sum;
-                }
-            }
-            __syncthreads();
-            write = set == 0;
-            if (write) {
-                for (int s = 1; s < sets; ++s) {
-                    const float m = lds_m[s * rows + row], next = fmaxf(top, m);
-                    const float f0 = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
-                    const float f1 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
-                    sum = sum * f0 + lds_l[s * rows + row] * f1;
-#pragma unroll
-                    for (int c = 0; c < VPL; ++c)
-                        acc[c] = acc[c] * f0 + buffers[(s * rows + row) * D + d0 + c] * f1;
-                    top = next;
-                }
-            }
-        }
-        if (write) {
+        // From here on 16 threads to a row, VPL values each, and the rows of all heads one
+        // after the other, 16 at a time.
+        const int rows = min(rq.n * a.group - tile * kRows, kRows), all = rows * spread;
+        const int mine = thread / 16, d0 = (thread & 15) * VPL;
+        const Parts parts(a);
+        const auto store = [&](int i, int row, float sum, const float *acc) {
             row += tile * kRows;
-            const int i = div_by(a.per_group, row), g = row - i * a.group;
-            const int64_t to = (int64_t)(rq.q0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs + d0;
+            const int token = div_by(a.per_group, row), g = row - token * a.group;
+            const int64_t to = (int64_t)(rq.q0 + token) * a.o_ts + (int64_t)((head + i) * a.group + g) * a.o_hs + d0;
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum; // no key seen: zeros
 #pragma unroll
             for (int c = 0; c < VPL; c += 4)
                 store4<BF, F32OUT>(a.out, to + c, f32x4{acc[c] * inv, acc[c + 1] * inv, acc[c + 2] * inv, acc[c + 3] * inv});
+        };
+        for (int at = mine; at < all; at += kRows) {
+            const int i = at / rows, row = at - i * rows, w0 = i * waves;
+            float top = kNegInf, sum = 0.0f, acc[VPL];
+#pragma unroll
+            for (int c = 0; c < VPL; ++c)
+                acc[c] = 0.0f;
+            for (int w = w0; w < w0 + waves; ++w)
+                top = fmaxf(top, lds_m[w * kRows + row]);
+            for (int w = w0; w < w0 + waves; ++w) {
+                const float mw = lds_m[w * kRows + row];
+                sum += lds_l[w * kRows + row] * (mw == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mw - top)); // keeps a NaN
+#pragma unroll
+                for (int c = 0; c < VPL; ++c)
+                    acc[c] += buffers[w * kBuffer + row * ROW + d0 + c];
+            }
+            if (sh.np == 1) {
+                store(i, row, sum, acc);
+            } else {
+                const int to = sh.part(sh.me) + i * kPart;
+#pragma unroll
+                for (int c = 0; c < VPL; c += 4)
+                    parts.put4(to + row * D + d0 + c, f32x4{acc[c], acc[c + 1], acc[c + 2], acc[c + 3]});
+                if (d0 == 0) {
+                    parts.put(to + kRows * D + row, top);
+                    parts.put(to + kRows * D + kRows + row, sum);
+                }
+            }
+        }
+        if (sh.np > 1 && last_part(a, sh, thread, &lds_last)) {
+            // what rows the tile lacks gives the others more threads, each set of them taking
+            // every sets-th part
+            const int sets = max(1, kRows / all);
+            for (int at0 = 0; at0 < all; at0 += kRows) {
+                const int set = sets == 1 ? 0 : mine / all, at = sets == 1 ? at0 + mine : mine - set * all;
+                const int i = at / rows, row = at - i * rows;
+                const bool on = set < sets && at < all;
+                float top = kNegInf, sum = 0.0f, acc[VPL];
+#pragma unroll
+                for (int c = 0; c < VPL; ++c)
+                    acc[c] = 0.0f;
+                if (on) {
+                    constexpr int kAhead = D == 256 ? 4 : 8; // parts on their way at once
+                    for (int i0 = set; i0 < sh.np; i0 += kAhead * sets) {
+                        float m[kAhead], s[kAhead];
+                        f32x4 x[kAhead][VPL / 4];
+#pragma unroll
+                        for (int u = 0; u < kAhead; ++u) {
+                            const int p = i0 + u * sets, from = sh.part(min(p, sh.np - 1)) + i * kPart;
+                            m[u] = parts.get(from + kRows * D + row);
+                            s[u] = parts.get(from + kRows * D + kRows + row);
+#pragma unroll
+                            for (int c = 0; c < VPL / 4; ++c)
+                                x[u][c] = parts.get4(from + row * D + d0 + 4 * c);
+                            if (p >= sh.np) {
+                                m[u] = kNegInf;
+                                s[u] = 0.0f;
+#pragma unroll
+                                for (int c = 0; c < VPL / 4; ++c)
+                                    x[u][c] = f32x4{0, 0, 0, 0};
+                            }
+                        }
+                        float next = top;
+#pragma unroll
+                        for (int u = 0; u < kAhead; ++u)
+                            next = fmaxf(next, m[u]);
+                        const float f0 = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
+                        sum *= f0;
+#pragma unroll
+                        for (int c = 0; c < VPL; ++c)
+                            acc[c] *= f0;
+#pragma unroll
+                        for (int u = 0; u < kAhead; ++u) {
+                            const float f = m[u] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[u] - next);
+                            sum += s[u] * f;
+#pragma unroll
+                            for (int c = 0; c < VPL; ++c)
+                                acc[c] += x[u][c / 4][c % 4] * f;
+                        }
+                        top = next;
+                    }
+                }
+                // join the sets: set 0 adds the others' in order.  They lie in the first
+                // buffer: at most 16 rows of VPL 16 floats, and their maxima and sums.
+                if (on && set > 0) {
+                    float *dst = buffers + (set * all + at) * D + d0;
+#pragma unroll
+                    for (int c = 0; c < VPL; c += 4)
+                        *reinterpret_cast<f32x4 *>(dst + c) = f32x4{acc[c], acc[c + 1], acc[c + 2], acc[c + 3]};
+                    if (d0 == 0) {
+                        lds_m[set * all + at] = top;
+                        lds_l[set * all + at] = sum;
+                    }
+                }
+                __syncthreads();
+                if (on && set == 0) {
+                    for (int s = 1; s < sets; ++s) {
+                        const float m = lds_m[s * all + at], next = fmaxf(top, m);
+                        const float f0 = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - next);
+                        const float f1 = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - next);
+                        sum = sum * f0 + lds_l[s * all + at] * f1;
+#pragma unroll
+                        for (int c = 0; c < VPL; ++c)
+                            acc[c] = acc[c] * f0 + buffers[(s * all + at) * D + d0 + c] * f1;
+                        top = next;
+                    }
+                    store(i, row, sum, acc);
+                }
+            }
         }
         __syncthreads(); // the buffers are free for the next share
     }
 };
 
-// Rounds: heads of 256 values have no registers for two blocks on their way and two in hand.
-constexpr int few_sub(int dim) { return dim == 256 ? 1 : 2; }
-
 template <int CODE, bool BF, int D, bool F32OUT, bool RUNS>
 __global__ __launch_bounds__(kThreads, 2) void paged8_few_kernel(Attn8Args)
 {
-    typedef FewTile<CODE, BF, D, F32OUT, RUNS, few_sub(D)> Tile;
+    typedef FewTile<CODE, BF, D, F32OUT, RUNS> Tile;
     __shared__ __align__(16) char lds[kWaves * Tile::kBuffer * sizeof(float)];
     run_plan<Tile>(lds);
 }

@@ -155,7 +155,7 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
 #pragma unroll
         for (int f = 0; f < kAsk; ++f) {
             const int row = own_row(f), turn = V ? v_turn(row) : k_turn(row), chunk = 2 * (lane % kPieces);
-            const float s = scale_of(raw.s[f]);
+            const Scale<CODE, BF> s(raw.s[f]);
             char *dst = to + row * kRowBytes;
             *reinterpret_cast<u32x4 *>(dst + 16 * (chunk ^ turn)) = widen8<CODE, BF>(raw.x[f][0], raw.x[f][1], s);
             *reinterpret_cast<u32x4 *>(dst + 16 * ((chunk + 1) ^ turn)) = widen8<CODE, BF>(raw.x[f][2], raw.x[f][3], s);
@@ -374,7 +374,7 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
             if (id < 0 || !sees(a, p_row, j))
                 continue;
             const uint8_t *src = at.template codes<true>(id, j) + values + 4 * half;
-            const float f = scale_of(*at.template scale<true>(id, j));
+            const Scale<CODE, BF> f(*at.template scale<true>(id, j));
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -399,7 +399,7 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyTile {
     static constexpr int kBuffer = Rows::kBlock * Rows::kRowBytes;
 
     // lds: two buffers for k and two for v, free again on return
-    static __device__ __forceinline__ void run(const Attn8Args &a, const Request &rq, int r, int tile, int head,
+    static __device__ __forceinline__ void run(const Attn8Args &a, const Request &rq, int r, int tile, int head, int,
                                                const Share &sh, char *lds)
     {
         constexpr int DT = Rows::DT, kBlock = Rows::kBlock;

@@ -61,11 +61,11 @@ template <int CODE, int TYPE> __global__ __launch_bounds__(kThreads) void paged8
             continue;
         u32x4 y = {0, 0, 0, 0};
         if (byte[i] >= 0) {
-            const float f = scale_of(byte[i]);
+            const Scale<CODE, TYPE == GEMV_W_BF16> scale(byte[i]);
             if constexpr (TYPE == GEMV_W_F32)
-                y = __builtin_bit_cast(u32x4, floats4<CODE>(w[i][0], f));
+                y = __builtin_bit_cast(u32x4, floats4<CODE>(w[i][0]) * scale.f);
             else
-                y = widen8<CODE, TYPE == GEMV_W_BF16>(w[i][0], w[i][E / 4 - 1], f);
+                y = widen8<CODE, TYPE == GEMV_W_BF16>(w[i][0], w[i][E / 4 - 1], scale);
         }
         char *const out = static_cast<char *>(v ? a.out[1] : a.out[0]);
         *reinterpret_cast<u32x4 *>(out + to[i] * (16 / E)) = y;
