@@ -65,7 +65,10 @@ extern "C" int gemv_paged8_attn(const void *q, int q_type, int64_t q_token_strid
     a.per_group = gemv::fast_div(a.group);
 
     const bool many = gemv::takes_many(tokens, requests, a.group);
-    const bool runs = cache->block % 8 == 0; // eight keys from a multiple of eight on lie in one page and share a scale
+    // where neighbouring keys lie: found once for all of a run, or key by key
+    const bool near = a.k_stride[1] < (1u << 27) && a.v_stride[1] < (1u << 27); // 16 rows' offsets stay below 2^31
+    const bool runs = !many ? cache->block % 8 == 0
+                            : near && cache->page_size % 16 == 0 && (cache->block % 16 == 0 || 16 % cache->block == 0);
     const bool f32out = out_type == GEMV_W_F32, bf = q_type == GEMV_W_BF16;
     const void *fn = cache->dim == 64    ? gemv::paged8_attn_kernel_64(cache->code, bf, f32out, runs, many)
                      : cache->dim == 128 ? gemv::paged8_attn_kernel_128(cache->code, bf, f32out, runs, many)

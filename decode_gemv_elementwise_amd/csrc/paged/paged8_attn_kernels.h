@@ -10,9 +10,11 @@ namespace {
 
 template <int CODE, bool BF, int D, bool F32OUT> const void *kernel_of(bool runs, bool many)
 {
-    return many   ? reinterpret_cast<const void *>(&paged8_many_kernel<CODE, BF, D, F32OUT>)
-           : runs ? reinterpret_cast<const void *>(&paged8_few_kernel<CODE, BF, D, F32OUT, true>)
-                  : reinterpret_cast<const void *>(&paged8_few_kernel<CODE, BF, D, F32OUT, false>);
+    if (many)
+        return runs ? reinterpret_cast<const void *>(&paged8_many_kernel<CODE, BF, D, F32OUT, true>)
+                    : reinterpret_cast<const void *>(&paged8_many_kernel<CODE, BF, D, F32OUT, false>);
+    return runs ? reinterpret_cast<const void *>(&paged8_few_kernel<CODE, BF, D, F32OUT, true>)
+                : reinterpret_cast<const void *>(&paged8_few_kernel<CODE, BF, D, F32OUT, false>);
 }
 
 template <int CODE, int D> const void *kernel_of(bool bf, bool f32out, bool runs, bool many)

@@ -55,7 +55,9 @@ __device__ __forceinline__ float half_sum(float v)
     return __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
 }
 
-template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
+// RUNS: 16 keys from a multiple of 16 on lie in one page, and a block of scales does not
+// begin or end within them, or is a power of two below 16.
+template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
     static constexpr int kBlock = many_block(D), KT = kBlock / 32; // keys of a block; tiles of 32 of them
     static constexpr int kRowBytes = 2 * D, kChunks = D / 8;      // 16-byte chunks of a row
     static constexpr int kOwn = kBlock / kWaves;                  // rows, next to each other, that a wave brings
@@ -78,6 +80,7 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
     int thread, lane, wave, col, half;
     int values; // first of the wave's values
     float scale;
+    uint32_t scale_row[RUNS ? kAsk : 1]; // blocks of scales between the wave's first row and the lane's
     uint32_t special; // not 0: an infinity or NaN of v was taken out
     u32x4 qf[KS];
     f32x16 o[DT];
@@ -85,16 +88,15 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
 
     __device__ ManyRows(const Attn8Args &args) : a(args) {}
 
-    // Where a row's chunk c lies: at chunk c ^ turn.  k is read 16 rows at a time,
-    // one chunk of each; v 4 rows at a time, 64 bytes of each.
+    // Where a row's chunk c lies: at place(c) ^ turn.  A lane writes chunks 2 i and 2 i + 1,
+    // eight lanes next to each other all 2 i at a time: those fill the row's first half.
+    // k is read 16 rows at a time, one chunk of each; v 4 rows at a time, 64 bytes of each.
+    static __device__ __forceinline__ int place(int c) { return (c >> 1) + (c & 1) * (kChunks / 2); }
     static __device__ __forceinline__ int k_turn(int row)
     {
         return (kRowBytes == 128 ? row >> 1 : row) & (kChunks < 16 ? kChunks - 1 : 15);
     }
-    static __device__ __forceinline__ int v_turn(int row)
-    {
-        return kRowBytes == 128 ? (row & 2) << 1 : (row & 3) << 2;
-    }
+    static __device__ __forceinline__ int v_turn(int row) { return kRowBytes == 128 ? row & 2 : (row & 3) << 1; }
 
     __device__ __forceinline__ void begin(const Request &rq, int r, int tile, int head)
     {
@@ -114,6 +116,11 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
         at.begin(a, r, head);
         scale = kept(a.scale_log2);
         special = 0;
+        if constexpr (RUNS) {
+#pragma unroll
+            for (int f = 0; f < kAsk; ++f)
+                scale_row[f] = div_by(at.block, f * kRun + lane / kPieces);
+        }
         p_row = -1;
         const int row = wrow + col;
         const int i = div_by(a.per_group, min(row, rows - 1)), g = min(row, rows - 1) - i * a.group;
@@ -141,6 +148,18 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
     // Asks for them; ids: the page of each lane's key.
     template <bool V> __device__ __forceinline__ void ask(int j0, int ids, Raw &raw) const
     {
+        if constexpr (RUNS) { // a wave's rows lie in one page, whose place is the same for all lanes
+            const int own = wave * kOwn, id = __builtin_amdgcn_readlane(ids, own);
+            const uint8_t *base = at.template codes<V>(id, j0 + own), *scales = at.template scale<V>(id, j0 + own);
+            const uint32_t step = V ? at.v1 : at.k1, sstep = V ? at.vs1 : at.ks1;
+            const uint32_t off = lane / kPieces * step + 16 * (lane % kPieces);
+#pragma unroll
+            for (int f = 0; f < kAsk; ++f) {
+                raw.x[f] = *reinterpret_cast<const u32x4 *>(base + (uint64_t)(f * kRun) * step + off);
+                raw.s[f] = scales[scale_row[f] * sstep];
+            }
+            return;
+        }
 #pragma unroll
         for (int f = 0; f < kAsk; ++f) {
             const int row = own_row(f), id = __shfl(ids, row);
@@ -154,11 +173,11 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
     {
 #pragma unroll
         for (int f = 0; f < kAsk; ++f) {
-            const int row = own_row(f), turn = V ? v_turn(row) : k_turn(row), chunk = 2 * (lane % kPieces);
+            const int row = own_row(f), chunk = lane % kPieces ^ (V ? v_turn(row) : k_turn(row));
             const Scale<CODE, BF> s(raw.s[f]);
             char *dst = to + row * kRowBytes;
-            *reinterpret_cast<u32x4 *>(dst + 16 * (chunk ^ turn)) = widen8<CODE, BF>(raw.x[f][0], raw.x[f][1], s);
-            *reinterpret_cast<u32x4 *>(dst + 16 * ((chunk + 1) ^ turn)) = widen8<CODE, BF>(raw.x[f][2], raw.x[f][3], s);
+            *reinterpret_cast<u32x4 *>(dst + 16 * chunk) = widen8<CODE, BF>(raw.x[f][0], raw.x[f][1], s);
+            *reinterpret_cast<u32x4 *>(dst + 16 * (chunk ^ kChunks / 2)) = widen8<CODE, BF>(raw.x[f][2], raw.x[f][3], s);
         }
     }
 
@@ -204,12 +223,12 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
         const char *k;
         int row, turn;
         __device__ __forceinline__ KAt(const char *k, int ln)
-            : k(k), row((ln & 31) * kRowBytes), turn(16 * ((ln >> 5) ^ k_turn(ln & 31)))
+            : k(k), row((ln & 31) * kRowBytes), turn(16 * (place(ln >> 5) ^ k_turn(ln & 31)))
         {
         }
         __device__ __forceinline__ u32x4 operator()(int n) const // rows 32 apart have the same turn
         {
-            return *reinterpret_cast<const u32x4 *>(k + (row + (turn ^ (32 * (n / KT)))) + n % KT * 32 * kRowBytes);
+            return *reinterpret_cast<const u32x4 *>(k + (row + (turn ^ (16 * (n / KT)))) + n % KT * 32 * kRowBytes);
         }
     };
     struct VAt {
@@ -219,12 +238,12 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
         __device__ __forceinline__ VAt(const char *v, int ln, int values) : v(v)
         {
             const int key = 4 * (ln >> 5) + ((ln & 15) >> 2), chunk = 2 * ((ln >> 4) & 1) + ((ln & 3) >> 1);
-            row = key * kRowBytes + 2 * values + 8 * (ln & 1);
-            turn = 16 * (chunk ^ v_turn(key));
+            row = key * kRowBytes + 8 * (ln & 1);
+            turn = 16 * ((place(chunk) + values / 16) ^ v_turn(key)); // 2 DT values / 16 at most: no bit of them meets
         }
         __device__ __forceinline__ u32x4 operator()(int n) const // rows 8 apart have the same turn
         {
-            const char *at = v + (row + (turn ^ (64 * (n % DT))));
+            const char *at = v + (row + (turn ^ (32 * (n % DT))));
             const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 16 * (n / DT) * kRowBytes));
             const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + (16 * (n / DT) + 8) * kRowBytes));
             const u32x2 lo = __builtin_bit_cast(u32x2, x), hi = __builtin_bit_cast(u32x2, y);
@@ -392,8 +411,8 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyRows {
 };
 
 // One share of a tile of many rows.
-template <int CODE, bool BF, int D, bool F32OUT> struct ManyTile {
-    typedef ManyRows<CODE, BF, D, F32OUT> Rows;
+template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyTile {
+    typedef ManyRows<CODE, BF, D, F32OUT, RUNS> Rows;
     static constexpr int kRows = many_rows(D), kPart = many_part(D);
     static constexpr uint32_t kLeast = D == 64 ? 16 : 8, kEdge = D == 64 ? 24 : D == 128 ? 12 : 8;
     static constexpr int kBuffer = Rows::kBlock * Rows::kRowBytes;
@@ -549,10 +568,10 @@ template <int CODE, bool BF, int D, bool F32OUT> struct ManyTile {
     }
 };
 
-template <int CODE, bool BF, int D, bool F32OUT>
+template <int CODE, bool BF, int D, bool F32OUT, bool RUNS>
 __global__ __launch_bounds__(kThreads, 2) void paged8_many_kernel(Attn8Args)
 {
-    typedef ManyTile<CODE, BF, D, F32OUT> Tile;
+    typedef ManyTile<CODE, BF, D, F32OUT, RUNS> Tile;
     __shared__ __align__(16) char lds[4 * Tile::kBuffer];
     run_plan<Tile>(lds);
 }

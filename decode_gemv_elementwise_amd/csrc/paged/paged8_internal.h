@@ -19,8 +19,10 @@ int validate_attn8(const void *q, int q_type, int64_t q_token_stride, int64_t q_
                    int64_t window, int64_t sinks, const void *out, int out_type, int64_t out_token_stride,
                    int64_t out_head_stride, const void *workspace, int64_t workspace_bytes);
 
-// The attention's kernel for heads of that many values.  runs: eight keys from a multiple
-// of eight on lie in one page and share a scale; many: row tiles of many rows.
+// The attention's kernel for heads of that many values.  many: row tiles of many rows.
+// runs: of few rows, that eight keys from a multiple of eight on lie in one page and share
+// a scale; of many, that 16 lie in one page, and a block of 16 or more holds all or none
+// of them, a shorter one divides 16.
 const void *paged8_attn_kernel_64(int code, bool bf, bool f32out, bool runs, bool many);
 const void *paged8_attn_kernel_128(int code, bool bf, bool f32out, bool runs, bool many);
 const void *paged8_attn_kernel_256(int code, bool bf, bool f32out, bool runs, bool many);
