@@ -13,8 +13,8 @@
 // block's scores.
 //
 // Codes come through registers, 16 bytes a lane: k's are asked for at a block's start
-// and widened into LDS between its two products, v's are asked for there and widened
-// at its end.  Two buffers for k and two for v, one barrier a block.  Which 16-byte
+// and widened into LDS among its products with v, v's are asked for between its two
+// products and widened at its end.  Two buffers for k and two for v, one barrier a block.  Which 16-byte
 // chunk of a row lies where is permuted by the row, so that the products' reads meet no
 // bank twice (k_turn, v_turn).
 //
@@ -168,17 +168,19 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
         }
     }
 
-    // Widens them into LDS.
+    // Widens them into LDS: one of 2 kAsk chunks, or all.
+    template <bool V> __device__ __forceinline__ void put(const Raw &raw, char *to, int i) const
+    {
+        const int f = i / 2, row = own_row(f), chunk = lane % kPieces ^ (V ? v_turn(row) : k_turn(row));
+        const Scale<CODE, BF> s(raw.s[f]);
+        *reinterpret_cast<u32x4 *>(to + row * kRowBytes + 16 * (i % 2 ? chunk ^ kChunks / 2 : chunk)) =
+            widen8<CODE, BF>(raw.x[f][i % 2 * 2], raw.x[f][i % 2 * 2 + 1], s);
+    }
     template <bool V> __device__ __forceinline__ void put(const Raw &raw, char *to) const
     {
 #pragma unroll
-        for (int f = 0; f < kAsk; ++f) {
-            const int row = own_row(f), chunk = lane % kPieces ^ (V ? v_turn(row) : k_turn(row));
-            const Scale<CODE, BF> s(raw.s[f]);
-            char *dst = to + row * kRowBytes;
-            *reinterpret_cast<u32x4 *>(dst + 16 * chunk) = widen8<CODE, BF>(raw.x[f][0], raw.x[f][1], s);
-            *reinterpret_cast<u32x4 *>(dst + 16 * (chunk ^ kChunks / 2)) = widen8<CODE, BF>(raw.x[f][2], raw.x[f][3], s);
-        }
+        for (int i = 0; i < 2 * kAsk; ++i)
+            put<V>(raw, to, i);
     }
 
     // Makes a block of v safe to multiply by weights of 0: keys past the tile's
@@ -228,7 +230,7 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
         }
         __device__ __forceinline__ u32x4 operator()(int n) const // rows 32 apart have the same turn
         {
-            return *reinterpret_cast<const u32x4 *>(k + (row + (turn ^ (16 * (n / KT)))) + n % KT * 32 * kRowBytes);
+            return *reinterpret_cast<const u32x4 *>(k + ((row + turn) ^ (16 * (n / KT))) + n % KT * 32 * kRowBytes);
         }
     };
     struct VAt {
@@ -243,7 +245,7 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
         }
         __device__ __forceinline__ u32x4 operator()(int n) const // rows 8 apart have the same turn
         {
-            const char *at = v + (row + (turn ^ (32 * (n % DT))));
+            const char *at = v + ((row + turn) ^ (32 * (n % DT)));
             const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 16 * (n / DT) * kRowBytes));
             const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + (16 * (n / DT) + 8) * kRowBytes));
             const u32x2 lo = __builtin_bit_cast(u32x2, x), hi = __builtin_bit_cast(u32x2, y);
@@ -287,10 +289,11 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
 
     // One block of keys whose scores are in s: their weights, formed while the
     // products of the next block (k there) run into `next`, then the sums over v.
-    // part: some rows do not see some of its keys.  between: work to do after the scores.
-    template <class F>
+    // part: some rows do not see some of its keys.  between: work to do after the scores;
+    // among(i): that of 2 kAsk pieces, spread over the products with v.
+    template <class F, class G>
     __device__ __forceinline__ void block(int j0, uint64_t has, const char *k, const char *v, bool part, f32x16 *s,
-                                          f32x16 *next, F between)
+                                          f32x16 *next, F between, G among)
     {
         if (part) {
             // by masks of all bits, not by comparisons: 32 of those would take 64 scalar registers
@@ -358,9 +361,7 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
                 }
             }
         });
-        __builtin_amdgcn_s_setprio(0);
         between();
-        __builtin_amdgcn_s_setprio(1);
         {
             constexpr int N = 2 * KT * DT;
             const VAt at(v, lane_here(), values);
@@ -376,6 +377,9 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
                     o[n % DT] = mfma32<BF>(f[n % kVAhead], pl[n / DT], o[n % DT]);
                 if (n + kVAhead < N)
                     f[n % kVAhead] = at(n + kVAhead);
+                constexpr int kEvery = N / (2 * kAsk);
+                if (n % kEvery == kEvery / 2)
+                    among(n / kEvery);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -462,26 +466,32 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyTile {
             const int j0 = key(b);
             __syncthreads(); // block b's v and b + 1's k are there; b's k and b - 1's v are done with
             const int id2 = t.at.checked(raw2);
-            typename Rows::Raw x;
-            if (b + 2 < b1)
-                t.template ask<false>(key(b + 2), id2, x);
+            // past the last block the last one's codes are widened again, and dropped
+            typename Rows::Raw x, y;
+            t.template ask<false>(key(min(b + 2, b1 - 1)), id2, x);
             raw2 = raw_at(b + 3);
             const auto between = [&] {
-                if (b + 2 < b1)
+                if constexpr (F32OUT) // both pieces of the weights leave no registers for x among the products
                     t.template put<false>(x, k);
-                if (b + 1 < b1)
-                    t.template ask<true>(key(b + 1), id1, x);
+                t.template ask<true>(key(min(b + 1, b1 - 1)), id1, y);
+            };
+            const auto among = [&](int i) {
+                if constexpr (!F32OUT)
+                    t.template put<false>(x, k, i);
             };
             // one body for both kinds of block: in two, the sums would be copied between them
             const bool part = !sees_all(a, t.p_lo, t.p_hi, j0, kBlock) || (has0 & kAll) != kAll;
             if (part)
                 t.clean(j0, has0, v);
-            if (t.live)
-                t.block(j0, has0, knext, v, part, s, next, between);
-            else
+            if (t.live) {
+                t.block(j0, has0, knext, v, part, s, next, between, among);
+            } else {
                 between();
-            if (b + 1 < b1)
-                t.template put<true>(x, vnext);
+#pragma unroll
+                for (int i = 0; i < 2 * Rows::kAsk; ++i)
+                    among(i);
+            }
+            t.template put<true>(y, vnext);
             has0 = has1;
             has1 = __ballot(id2 >= 0);
             id1 = id2;
