@@ -393,10 +393,10 @@ __device__ __forceinline__ void write_token(const Append8Args &a, const Run &r, 
     put16(a, to.codes + (r.slot - r.block * (int)a.block.d) * to.place, p, x, inverse_of(b));
 }
 
-// The wide path: 16-byte vectors of whole rows.  PP: tokens that a lane holds values of;
-// TEAM: waves that hold a run's head together.  A run of more tokens than that (two of one
-// slot are in it) is taken in parts.
-template <class S, bool PAIRS, int PP, int TEAM>
+// The wide path: 16-byte vectors of whole rows.  PP: tokens that a lane holds values of, so
+// that four waves hold a whole block's.  A run of more tokens than that (two of one slot
+// are in it) is taken in parts.
+template <class S, bool PAIRS, int PP>
 __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
 {
     extern __shared__ float2 turns[];
@@ -410,29 +410,31 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
     const int sub = div_by(a.items, lane), item = lane - sub * a.items.d;
     const int per = kWave / (int)a.items.d; // tokens of a wave at a time
     const Place kq = place_of<PAIRS>(a, item), plain{16 * item, 16 * item + 8};
-    const int team = wave / TEAM, me = wave % TEAM;
     __shared__ uint32_t largest[2][kWaves];
     int turned = 0; // which half of `largest`
-    int dealt = 0, dealt_tokens = 0; // rows given to teams, and pieces of single tokens' rows to waves, so far
+    int dealt = 0; // rows, or pieces of single tokens' rows, given out so far
     each_run(a, group_here(), [&](const Run &r, int share) {
         const int row0 = share * a.kv_share, end = min(row0 + a.kv_share, 2 * a.heads);
         if (r.n == 1 && (a.items.d & (a.items.d - 1)) == 0) {
             const int pieces = (end - row0 + per - 1) / per;
-            for (int i = (wave - dealt_tokens) & (kWaves - 1); i < pieces; i += kWaves)
+            for (int i = (wave - dealt) & (kWaves - 1); i < pieces; i += kWaves)
                 write_token<S, PAIRS>(a, r, row0 + i * per + sub, end, item);
-            dealt_tokens += pieces;
+            dealt += pieces;
             return;
         }
-        const int most = TEAM * PP * per;
+        const int most = kWaves * PP * per;
         for (int left = r.n; left > 0; left -= most) {
             const int from = r.first + (r.n - left), n = min(left, most);
+            // waves that hold a head together, a team; their teams take heads in turn
+            const int waves = n <= PP * per ? 1 : n <= 2 * PP * per ? 2 : kWaves, teams = kWaves / waves;
+            const int team = wave / waves, me = wave & (waves - 1);
             const bool begun = r.begun && from == r.first;
             uint32_t t[PP];
             int place[PP];
             bool live[PP];
 #pragma unroll
             for (int i = 0; i < PP; ++i) {
-                const int off = (i * TEAM + me) * per + sub;
+                const int off = (i * waves + me) * per + sub;
                 t[i] = (uint32_t)from + off;
                 live[i] = sub < per && off < n;
                 place[i] = live[i] ? a.slots[t[i]] - r.block * (int)a.block.d : 0;
@@ -449,10 +451,8 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
                     if (live[i])
                         raw[i].load(src + (int64_t)t[i] * stride, p.lo, p.hi);
             };
-            constexpr int kTeams = kWaves / TEAM;
-            int row = row0 + ((team - dealt) & (kTeams - 1));
-            if constexpr (TEAM == 1)
-                dealt += end - row0;
+            int row = row0 + ((team - dealt) & (teams - 1));
+            dealt += end - row0;
             if (row < end)
                 load(row);
 #pragma unroll
@@ -460,7 +460,7 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
                 if (row < a.heads && live[i]) // a first row of v: so are the others
                     turns_of(a, t[i], item, turn[i]);
             // teams of several waves go through as many rounds each: they meet in every one
-            for (int left_rows = end - row0; TEAM == 1 ? row < end : left_rows > 0; row += kTeams, left_rows -= kTeams) {
+            for (int rounds = (end - row0 + teams - 1) / teams; waves == 1 ? row < end : rounds > 0; row += teams, --rounds) {
                 const bool on = row < end;
                 const int v = row >= a.heads, head = v ? row - a.heads : row;
                 const Place p = v ? plain : kq;
@@ -478,24 +478,23 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
                             turn16<PAIRS>(a, item, turn[i], x[i]);
                         top = largest_of(x[i], top);
                     }
-                if (row + kTeams < end)
-                    load(row + kTeams); // on its way while this one is written
+                if (row + teams < end)
+                    load(row + teams); // on its way while this one is written
                 top = wave_max(top);
-                if constexpr (TEAM > 1) {
+                if (waves > 1) {
                     if (lane == 0)
                         largest[turned][wave] = top;
                     asm volatile("" ::"v"(old)); // read by all before one of them writes the new one
                     meet();
-#pragma unroll
-                    for (int w = 0; w < TEAM; ++w)
-                        top = max(top, largest[turned][team * TEAM + w]);
+                    for (int w = 0; w < waves; ++w)
+                        top = max(top, largest[turned][team * waves + w]);
                     turned ^= 1; // the next head's go where none reads any more
                     if (!on)
                         continue;
                 }
                 const int b = begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
                 if (!begun && b > old && b < 255)
-                    rescale(a, r, to, old, b, me * kWave + lane, TEAM * kWave);
+                    rescale(a, r, to, old, b, me * kWave + lane, waves * kWave);
                 const float inv = inverse_of(b);
                 if (me == 0 && lane == 0)
                     *to.scale = (uint8_t)b;
@@ -570,14 +569,12 @@ template <class S> __global__ __launch_bounds__(kThreads) void paged8_append_gen
     });
 }
 
-// passes: tokens that a lane has to hold for a whole block, 0 for what the wide path does not take.
+// passes: tokens that a lane of one wave would hold of a whole block, 0 for what the wide path does not take.
 template <class S, bool PAIRS> const void *kernel_of(int passes)
 {
-    return passes <= 1   ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 1, 1>)
-           : passes <= 2 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 1, 2>)
-           : passes <= 4 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 1, 4>)
-           : passes <= 8 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 2, 4>)
-                         : reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 4, 4>);
+    return passes <= 4   ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 1>)
+           : passes <= 8 ? reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 2>)
+                         : reinterpret_cast<const void *>(&paged8_append_kernel<S, PAIRS, 4>);
 }
 
 template <class S> const void *kernel_of(bool pairs, int passes)
@@ -626,18 +623,18 @@ extern "C" int gemv_paged8_append(const void *q, const void *k, const void *v, i
         wide = wide && reinterpret_cast<uintptr_t>(a.src[i]) % 16 == 0 && a.src_stride[i] * size % 16 == 0;
     const int items = cache->dim / 16, per = gemv::kWave / items; // lanes of a token's head, tokens of a wave at a time
     a.items = gemv::fast_div(items);
-    int64_t passes = (cache->block + per - 1) / per; // tokens that a lane holds of a whole block
+    int64_t passes = (cache->block + per - 1) / per; // tokens that a lane of one wave would hold of a whole block
     if (!wide || passes > 16)
         passes = 0;
 
     // Some thousand workgroups for k and v, each for four rows (one a wave) of a stretch of
     // tokens: of a chunk few begin a run, and more rows would be taken one after the other
-    // (8192 tokens, blocks of 64: 38 us with 4 rows, 43 with 8, 52 with 16; 512 tokens 10,
-    // 15, 15).  Where the tokens are many and a wave or two hold a block's, eight: fewer
-    // workgroups form the same angles, and single tokens' rows fill a wave (8192 tokens in
-    // blocks of 16 40 us, 44 with 4 rows; 4096 single tokens 24 and 34).
+    // (8192 tokens, blocks of 64: 33 us with 4 rows, 40 with 8; 512 tokens 10 and 15).  Where
+    // the tokens are many and a wave or two hold a block's, eight: fewer workgroups form the
+    // same angles, and single tokens' rows fill a wave (8192 tokens in blocks of 16 40 us,
+    // 44 with 4 rows; 4096 single tokens 25 and 34; 1024 tokens of one chunk 18 and 14).
     const int64_t rows = 2 * (int64_t)a.heads;
-    int64_t kv_share = tokens >= 2048 && passes <= 2 ? 8 : 4;
+    int64_t kv_share = tokens >= 1024 && passes <= 2 ? 8 : 4;
     int64_t stretch = tokens * ((rows + kv_share - 1) / kv_share) / 1024;
     stretch = stretch < 1 ? 1 : stretch < 32 ? stretch : 32;
     const int64_t per_die = ((tokens + stretch - 1) / stretch + 7) / 8, stretches = 8 * per_die;

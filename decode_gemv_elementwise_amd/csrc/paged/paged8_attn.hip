@@ -8,14 +8,17 @@ namespace gemv {
 namespace {
 
 // Which kind of row tile a call takes.  The host knows the counts of tokens and requests
-// and no lengths: tiles of few rows where a request has one token, or up to 16 rows, on
-// average; but with more tokens than kFewTokens only the first, for a long chunk among
-// them would read its keys again for every 16 rows.
+// and no lengths: tiles of few rows where a request has one token, or up to 48 rows (three
+// such tiles, which read its keys three times), on average; but with more tokens than
+// kFewTokens only the first, for a long chunk among them would read its keys again for
+// every 16 rows.  8 requests of 8 tokens, 4 heads a group (32 rows), over up to 16000 keys:
+// heads of 64 38 us by few rows, 47 by many; of 128 48 and 59; of 256 107 and 96 (over up to
+// 2500 keys 19 and 30, 21 and 28, 38 and 38).
 constexpr int64_t kFewTokens = 256;
 
 bool takes_many(int64_t tokens, int64_t requests, int64_t group)
 {
-    return tokens > requests && (tokens * group > kAttnRows * requests || tokens > kFewTokens);
+    return tokens > requests && (tokens * group > 3 * kAttnRows * requests || tokens > kFewTokens);
 }
 
 } // namespace
