@@ -1,8 +1,9 @@
 """One attention block of a decode layer over a paged cache, served in steps.
 
-    python examples/paged_decode.py
+    python examples/paged_decode.py [int8 | e4m3]
 
-A step takes up to eight tokens of any requests: chunks of new prompts, single
+With an argument the cache is held in 8 bits, half the bytes, with a scale for each
+page and head.  A step takes up to eight tokens of any requests: chunks of new prompts, single
 tokens, or both.  Five launches run it: the qkv product of all columns, the block
 tables and slot maps from the requests' lengths, rotary positions with the write
 into the cache, attention over the cache, and the output product with the residual.
@@ -17,16 +18,17 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from decode_gemv_elementwise_amd import binding, paged, synth  # noqa: E402
+from decode_gemv_elementwise_amd import binding, paged, paged8, synth  # noqa: E402
 
 COLUMNS = 8  # tokens of a step: what one product call takes
 
 
 class Block:
-    """Weights and buffers; ``hidden`` values a token, heads of ``dim`` values."""
+    """Weights and buffers; ``hidden`` values a token, heads of ``dim`` values; ``codes``: None for a cache of bfloat16, or
+    "int8" or "e4m3"."""
 
     def __init__(self, hidden=4096, heads=32, kv_heads=8, dim=128, page=16, pages=256, requests=4, longest=1024, window=0,
-                 sinks=0, seed=0):
+                 sinks=0, seed=0, codes=None):
         rng = np.random.default_rng(seed)
         self.hidden, self.heads, self.kv_heads, self.dim, self.page = hidden, heads, kv_heads, dim, page
         self.window, self.sinks, self.longest = window, sinks, longest
@@ -40,7 +42,12 @@ class Block:
         self.x, self.qkv, self.mixed, self.y = (floats(COLUMNS, hidden), floats(COLUMNS, self.rows),
                                                 floats(COLUMNS, heads, dim), floats(COLUMNS, hidden))
         self.q = torch.zeros(COLUMNS, heads, dim, dtype=torch.bfloat16, device=dev)
-        self.k_cache, self.v_cache = (torch.zeros(pages, page, kv_heads, dim, dtype=torch.bfloat16, device=dev) for _ in "kv")
+        self.codes = codes
+        if codes is None:
+            self.cache = tuple(torch.zeros(pages, page, kv_heads, dim, dtype=torch.bfloat16, device=dev) for _ in "kv")
+        else:
+            self.cache = paged8.cache(pages, page, kv_heads, dim, codes, device=dev)
+        self.k_cache, self.v_cache = self.cache[:2]
         self.inv_freq = (10000.0 ** (-torch.arange(dim // 2, dtype=torch.float64) / (dim // 2))).float().to(dev)
         self.cached, self.fresh = ints(requests), ints(requests)
         self.table = torch.full((requests, -(-longest // page)), -1, dtype=torch.int32, device=dev)
@@ -58,10 +65,12 @@ class Block:
         paged.gemv_paged_slots(self.cached, self.fresh, self.free, self.page, self.table, self.query_start, self.kv_len,
                                self.request, self.positions, self.slots, self.used)
         q, k, v = self.qkv.split([self.heads * d, self.kv_heads * d, self.kv_heads * d], 1)
-        paged.gemv_paged_append(q.unflatten(1, (-1, d)), k.unflatten(1, (-1, d)), v.unflatten(1, (-1, d)), self.positions,
-                                self.inv_freq, self.slots, self.q, self.k_cache, self.v_cache)
-        paged.gemv_paged_attn(self.q, self.k_cache, self.v_cache, self.table, self.query_start, self.kv_len, d ** -0.5,
-                              self.mixed, self.workspace, window=self.window, sinks=self.sinks)
+        append, attn = ((paged.gemv_paged_append, paged.gemv_paged_attn) if self.codes is None else
+                        (paged8.gemv_paged8_append, paged8.gemv_paged8_attn))
+        append(q.unflatten(1, (-1, d)), k.unflatten(1, (-1, d)), v.unflatten(1, (-1, d)), self.positions, self.inv_freq,
+               self.slots, self.q, *self.cache)
+        attn(self.q, *self.cache, self.table, self.query_start, self.kv_len, d ** -0.5, self.mixed, self.workspace,
+             window=self.window, sinks=self.sinks)
         binding.gemv_fused_ncols(self.out_data, "bf16", self.hidden, self.heads * d, t, self.mixed, "add",
                                  add_operand=self.x, dst=self.y)
 
@@ -84,10 +93,10 @@ class Block:
             self.launches()
         else:
             if self.graph is None:
-                saved = [t.clone() for t in (self.table, self.k_cache, self.v_cache)]
+                saved = [t.clone() for t in (self.table, *self.cache)]
                 self.launches()  # once outside: the library loads its code
                 torch.cuda.synchronize()
-                for t, s in zip((self.table, self.k_cache, self.v_cache), saved):
+                for t, s in zip((self.table, *self.cache), saved):
                     t.copy_(s)
                 self.graph = torch.cuda.CUDAGraph()
                 with torch.cuda.graph(self.graph):
@@ -104,8 +113,8 @@ class Block:
         self.lengths[request] = 0
 
 
-def main():
-    block = Block()
+def main(codes=None):
+    block = Block(codes=codes)
     g = torch.Generator(device="cuda").manual_seed(0)
     tokens = lambda n: torch.randn(n, block.hidden, generator=g, device="cuda")  # noqa: E731
     for fresh in ([8, 0, 0, 0], [1, 7, 0, 0], [1, 1, 6, 0], [1, 1, 1, 5]):
@@ -125,4 +134,4 @@ def main():
 
 
 if __name__ == "__main__":
-    main()
+    main(*sys.argv[1:2])
