@@ -92,7 +92,7 @@ template <bool PAIRS> __device__ __forceinline__ Place place_of(const Append8Arg
 __device__ __forceinline__ float2 turn_at(const Append8Args &a, int t, int pair)
 {
     const int ax = a.axis ? a.axis[pair] : 0;
-    return (unsigned)ax < (unsigned)a.axes ? turn_of(a.positions[(int64_t)ax * a.tokens + t], a.inv_freq[pair])
+    return (unsigned)ax < (unsigned)a.axes ? turn_close(a.positions[(int64_t)ax * a.tokens + t], a.inv_freq[pair])
                                            : float2{1.0f, 0.0f};
 }
 
