@@ -429,6 +429,7 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
             const int waves = n <= PP * per ? 1 : n <= 2 * PP * per ? 2 : kWaves, teams = kWaves / waves;
             const int team = wave / waves, me = wave & (waves - 1);
             const bool begun = r.begun && from == r.first;
+            const Run part{from, n, r.block, r.slot, begun, r.straight && n == r.n};
             uint32_t t[PP];
             int place[PP];
             bool live[PP];
@@ -494,7 +495,7 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
                 }
                 const int b = begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
                 if (!begun && b > old && b < 255)
-                    rescale(a, r, to, old, b, me * kWave + lane, waves * kWave);
+                    rescale(a, part, to, old, b, me * kWave + lane, waves * kWave);
                 const float inv = inverse_of(b);
                 if (me == 0 && lane == 0)
                     *to.scale = (uint8_t)b;
@@ -657,9 +658,8 @@ extern "C" int gemv_paged8_append(const void *q, const void *k, const void *v, i
     q_share = q_share < q_items ? q_share : q_items;
     while (q_groups * ((q_items + q_share - 1) / q_share) > gemv::kMostGroups && q_share < q_items)
         q_share *= 2;
+    // below 2^31: of at most 2^30 tokens up to 2^30 for q (one a token), and 2^29 for k and v
     const int64_t q_shares = (q_items + q_share - 1) / q_share, groups = kv_groups + q_groups * q_shares;
-    if (groups > INT_MAX) // rows of a stride of 0 for more tokens and heads than any memory holds
-        return GEMV_E_DIM;
     a.q_share = (int)q_share, a.q_tokens = (int)q_tokens, a.q_items = gemv::fast_div(q_items);
     a.q_shares = gemv::fast_div(q_shares), a.kv_shares = gemv::fast_div(kv_shares);
     a.kv_groups = (int)kv_groups, a.groups = (int)groups;

@@ -324,3 +324,24 @@ def test_wrong_tensors_are_refused():
         paged8.gemv_paged8_read(*c.c.all, i3, x, x)
     torch.cuda.synchronize()
     assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("code", ref.CODES)
+def test_append_slot_many_times(code):
+    """A slot many times over with values that grow: its block's other new tokens keep theirs."""
+    n = 300
+    c = Cache(code, 4, 16, 16, 2, 64, seed=1)
+    before = c.copy()
+    x = torch.randn(n, 2, 64, device="cuda") * torch.exp2(torch.arange(n, device="cuda") / 32.0)[:, None, None]
+    slots = [21, 22, 23] + [25] * (n - 3)
+    out = torch.empty(n, 2, 64, device="cuda", dtype=torch.bfloat16)
+    paged8.gemv_paged8_append(x, x, x, ints([0] * n), torch.empty(0, device="cuda"), ints(slots), out, *c.all)
+    for codes, byte, old, old_byte in ((c.k, c.ks, before[0], before[2]), (c.v, c.vs, before[1], before[3])):
+        got, old = ref.values(codes, byte), ref.values(old, old_byte)
+        step = ref.scales(byte.cpu())[1, 0][:, None]
+        rest = [p for p in range(16) if p not in (5, 6, 7, 9)]
+        for mine, want in ((got[1, 5:8], x[:3].double().cpu()), (got[1, rest], old[1, rest])):
+            # each rounding, at scales that at least double: below a step of the last; for e4m3 2^-4 of the value at the
+            # first and steps of 2^-9 after it
+            tol = step if code == "int8" else 2.0 ** -4 * want.abs() + 2.0 ** -9 * step
+            assert ((mine - want).abs() <= tol).all()
