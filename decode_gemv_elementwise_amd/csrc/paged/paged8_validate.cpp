@@ -101,7 +101,7 @@ int validate_append8(const void *q, const void *k, const void *v, int src_type, 
         return GEMV_E_FMT;
     if (style != GEMV_ROPE_HALVES && style != GEMV_ROPE_PAIRS)
         return GEMV_E_ACT;
-    if (tokens < 0 || tokens > kInt || q_heads < 1 || q_heads > GEMV_PAGED_MAX_HEADS || axes < 1 || axes > 64 ||
+    if (tokens < 0 || tokens > kInt / 2 + 1 || q_heads < 1 || q_heads > GEMV_PAGED_MAX_HEADS || axes < 1 || axes > 64 ||
         rot < 0 || rot > cache->dim || rot % 2 != 0)
         return GEMV_E_DIM;
     const int64_t qrow = q_heads * cache->dim, krow = (int64_t)cache->heads * cache->dim;

@@ -74,8 +74,8 @@ typedef struct {
  * neighbours in the call (in any order), as gemv_paged_slots lays them out; where
  * others lie between them, that block's values are unspecified.  Two tokens of one slot
  * leave either's values, and those of their block may be rounded twice.
- *  q, k, v, src_type, positions, axes, axis, inv_freq, rot, style, slots
- *              as for gemv_paged_append.
+ *  q, k, v, src_type, tokens, positions, axes, axis, inv_freq, rot, style, slots
+ *              as for gemv_paged_append, tokens up to 2^30.
  *  q_out       [tokens][q_heads][dim], contiguous, 16-byte aligned.
  * q_out, the codes and the scales overlap no input and not one another.
  * 16-byte aligned rows with strides of whole 16 bytes, and rot a multiple of 16
@@ -110,12 +110,14 @@ int gemv_paged8_read_validate(const gemv_kv_cache8 *cache, const int32_t *slots,
                               const void *v_out, int out_type, int64_t k_out_stride, int64_t v_out_stride);
 
 /* Attention of every request's new tokens over its paged cache: gemv_paged_attn
- * with k_j and v_j the cache's values rounded once to q's type, and every argument
- * as there but for
+ * with k_j and v_j the cache's values, and every argument as there but for
  *  q_type      GEMV_W_F16 or GEMV_W_BF16: q's, and out's where that is not f32.
  *  cache       dim 64, 128 or 256.
  *  workspace   that of gemv_paged_attn (gemv_paged_attn_workspace); one may serve both.
- * Blocks of whole multiples of 8 tokens take the wide path; others are found key by key. */
+ * A value that q's type does not hold (only binary16 has such) enters as it is or rounded
+ * to that type.  Wide paths are for blocks of whole multiples of 8 tokens (calls
+ * of few tokens a request) and for pages of whole multiples of 16 whose blocks divide or
+ * are divided by 16 (calls of many); others find each key by itself. */
 int gemv_paged8_attn(const void *q, int q_type, int64_t q_token_stride, int64_t q_head_stride,
                      const gemv_kv_cache8 *cache, const int32_t *block_table, int64_t table_width,
                      int64_t table_stride, const int32_t *query_start, const int32_t *kv_len, int64_t requests,

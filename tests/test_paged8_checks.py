@@ -71,7 +71,7 @@ def test_append_accepts():
 @pytest.mark.parametrize("change,want", [
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(pos=None), NULL), (dict(inv=None), NULL),
     (dict(slots=None), NULL), (dict(out=None), NULL), (dict(src=3), FMT), (dict(src=-1), FMT), (dict(type=0), FMT),
-    (dict(type=3), FMT), (dict(style=2), ACT), (dict(style=-1), ACT), (dict(tokens=-1), DIM), (dict(tokens=1 << 31), DIM),
+    (dict(type=3), FMT), (dict(style=2), ACT), (dict(style=-1), ACT), (dict(tokens=-1), DIM), (dict(tokens=1 << 31), DIM), (dict(tokens=(1 << 30) + 1), DIM),
     (dict(q_heads=0), DIM), (dict(q_heads=4097), DIM), (dict(axes=0), DIM), (dict(axes=65), DIM), (dict(rot=-2), DIM),
     (dict(rot=130), DIM), (dict(rot=127), DIM), (dict(qs=-1), LAYOUT), (dict(ks=1 << 31), LAYOUT), (dict(vs=-8), LAYOUT),
     (dict(q=16 * MB + 2), ALIGN), (dict(src=2, k=32 * MB + 1), ALIGN), (dict(pos=64 * MB + 2), ALIGN), (dict(out=80 * MB + 8), ALIGN),
