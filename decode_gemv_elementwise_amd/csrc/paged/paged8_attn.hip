@@ -8,17 +8,17 @@ namespace gemv {
 namespace {
 
 // Which kind of row tile a call takes.  The host knows the counts of tokens and requests
-// and no lengths: tiles of few rows where a request has one token, or up to 48 rows (three
-// such tiles, which read its keys three times), on average; but with more tokens than
-// kFewTokens only the first, for a long chunk among them would read its keys again for
-// every 16 rows.  8 requests of 8 tokens, 4 heads a group (32 rows), over up to 16000 keys:
-// heads of 64 38 us by few rows, 47 by many; of 128 48 and 59; of 256 107 and 96 (over up to
-// 2500 keys 19 and 30, 21 and 28, 38 and 38).
-constexpr int64_t kFewTokens = 256;
-
+// and no lengths.  A pass of 16 rows over a request's keys is bound by memory the first
+// time and costs 0.4 to 0.8 of that again; one of 128 rows costs 1.4, for its products.  So
+// few rows where a request has two such passes of 16 or less on average, spread evenly or
+// all in one chunk.  Heads of 128 in e4m3, 4 a group, over 4096 keys: 8 requests of 4 tokens
+// 24 us by few rows, 27 by many, of 8 tokens 28 and 28, of 9 49 and 34; 128 of 4 tokens 215
+// and 285; 128 of one token and a chunk of 256 over 2048 keys 135 and 184, 32 and such a
+// chunk 66 and 68.  One request of 8 tokens over 32768 keys: 40 and 53; heads of 64 33 and
+// 51, of 256 92 and 87.
 bool takes_many(int64_t tokens, int64_t requests, int64_t group)
 {
-    return tokens > requests && (tokens * group > 3 * kAttnRows * requests || tokens > kFewTokens);
+    return tokens > requests && tokens * group > 2 * kAttnRows * requests;
 }
 
 } // namespace
