@@ -69,7 +69,9 @@ extern "C" int gemv_paged8_attn(const void *q, int q_type, int64_t q_token_strid
 
     const bool many = gemv::takes_many(tokens, requests, a.group);
     // where neighbouring keys lie: found once for all of a run, or key by key
-    const bool near = a.k_stride[1] < (1u << 27) && a.v_stride[1] < (1u << 27); // 16 rows' offsets stay below 2^31
+    // 16 rows' offsets, and those of their scales, stay below 2^31
+    const bool near = a.k_stride[1] < (1u << 27) && a.v_stride[1] < (1u << 27) && a.ks_stride[1] < (1u << 27) &&
+                      a.vs_stride[1] < (1u << 27);
     const bool runs = !many ? cache->block % 8 == 0
                             : near && cache->page_size % 16 == 0 && (cache->block % 16 == 0 || 16 % cache->block == 0);
     const bool f32out = out_type == GEMV_W_F32, bf = q_type == GEMV_W_BF16;

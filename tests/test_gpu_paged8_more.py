@@ -345,3 +345,16 @@ def test_append_slot_many_times(code):
             # first and steps of 2^-9 after it
             tol = step if code == "int8" else 2.0 ** -4 * want.abs() + 2.0 ** -9 * step
             assert ((mine - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("lens", [[(40, 90), (1, 33)], [(1, 70), (1, 90)]])
+def test_scales_of_a_page_far_apart(lens):
+    """Neighbouring blocks' scales 300 million bytes apart: a page's sixteen span more than 32 bits."""
+    c = Case(lens, "int8", "bf16", 2, 1, 64, block=1, seed=5)
+    pages, step = c.c.ks.shape[0], 300_000_000
+    room = torch.zeros(16 * step, dtype=torch.uint8, device="cuda")
+    for i, name in enumerate(("ks", "vs")):
+        far = room[i * pages:].as_strided((pages, 16, 1), (1, step, 1))
+        far.copy_(getattr(c.c, name))
+        setattr(c.c, name, far)
+    c.check(c.run())
