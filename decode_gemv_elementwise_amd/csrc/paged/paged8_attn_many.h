@@ -14,9 +14,9 @@
 //
 // Codes come through registers, 16 bytes a lane: k's are asked for at a block's start
 // and widened into LDS among its products with v, v's are asked for between its two
-// products and widened at its end.  Two buffers for k and two for v, one barrier a block.  Which 16-byte
-// chunk of a row lies where is permuted by the row, so that the products' reads meet no
-// bank twice (k_turn, v_turn).
+// products and widened at its end, in the same step or (kDeep) the next.  Two buffers for k
+// and two for v, one barrier a block.  Which 16-byte chunk of a row lies where is permuted
+// by the row, so that the products' reads meet no bank twice (k_turn, v_turn).
 //
 // The running maximum only moves when a row's new one is more than kSlack above it:
 // most blocks then skip the pass over the 32 x D sums.  A weight may then be up to
@@ -418,8 +418,12 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
 template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyTile {
     typedef ManyRows<CODE, BF, D, F32OUT, RUNS> Rows;
     static constexpr int kRows = many_rows(D), kPart = many_part(D);
-    static constexpr uint32_t kLeast = D == 64 ? 16 : 8, kEdge = D == 64 ? 24 : D == 128 ? 12 : 8;
+    static constexpr uint32_t kLeast = D == 64 ? 16 : 8, kEdge = 8;
     static constexpr int kBuffer = Rows::kBlock * Rows::kRowBytes;
+    // Codes are on their way for a step more where there are registers: 2048 tokens over 8192
+    // keys of heads of 64 189 to 181 us, 64 over 32768 63 to 57; of 256 166 to 162.  Heads of
+    // 128 have none left (273 to 285).
+    static constexpr int kDeep = D == 128 ? 0 : 1;
 
     // lds: two buffers for k and two for v, free again on return
     static __device__ __forceinline__ void run(const Attn8Args &a, const Request &rq, int r, int tile, int head, int,
@@ -436,70 +440,85 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyTile {
 
         const auto key = [&](int b) { return walk.block(b) * kBlock; };
         // Block b's scores are formed during block b - 1, so its k is widened two blocks
-        // ahead and its v one.  id1: checked pages of block b + 1's keys (a lane's key
-        // each), raw2: of block b + 2's as the table has them, so that their load is
-        // waited for where they are used; has0, has1: which keys of b and b + 1 have one.
+        // ahead and its v one; both are asked for kDeep blocks before.  idm: checked pages of
+        // block b + kDeep + 1's keys (a lane's key each), raw: of the next block's as the table
+        // has them, so that their load is waited for where they are used; has: which keys of b
+        // and the blocks after it have one.
         const auto raw_at = [&](int b) { return b < b1 ? t.at.raw(key(b) + t.lane) : -1; };
-        int id1 = t.at.checked(raw_at(b0)), raw2 = raw_at(b0 + 1);
-        uint64_t has0 = __ballot(id1 >= 0), has1 = 0;
+        const auto last = [&](int b) { return key(min(b, b1 - 1)); }; // past the last block its codes are widened again, and dropped
+        uint64_t has[kDeep + 2];
+        int idm = 0, raw = 0;
         f32x16 sa[Rows::KT], sb[Rows::KT];
+        typename Rows::Raw x[kDeep + 1], y[kDeep + 1];
         if (b0 < b1) {
-            typename Rows::Raw x, y;
-            t.template ask<false>(key(b0), id1, x);
-            t.template ask<true>(key(b0), id1, y);
-            id1 = t.at.checked(raw2);
-            has1 = __ballot(id1 >= 0);
-            raw2 = raw_at(b0 + 2);
-            t.template put<false>(x, ka);
-            t.template put<true>(y, va);
-            if (b0 + 1 < b1) {
-                t.template ask<false>(key(b0 + 1), id1, x);
-                t.template put<false>(x, kb);
+            int ids[kDeep + 2];
+#pragma unroll
+            for (int i = 0; i < kDeep + 2; ++i)
+                ids[i] = raw_at(b0 + i);
+            raw = raw_at(b0 + kDeep + 2);
+#pragma unroll
+            for (int i = 0; i < kDeep + 2; ++i) {
+                ids[i] = t.at.checked(ids[i]);
+                has[i] = __ballot(ids[i] >= 0);
             }
+            typename Rows::Raw z, u;
+            t.template ask<false>(key(b0), ids[0], z);
+            t.template ask<true>(key(b0), ids[0], u);
+            t.template put<false>(z, ka);
+            t.template put<true>(u, va);
+            t.template ask<false>(last(b0 + 1), ids[1], z);
+            if constexpr (kDeep) {
+                t.template ask<false>(last(b0 + 2), ids[kDeep + 1], x[0]);
+                t.template ask<true>(last(b0 + 1), ids[1], y[0]);
+            }
+            t.template put<false>(z, kb);
+            idm = ids[kDeep + 1];
             __syncthreads();
             t.scores(ka, sa, [](int) {});
         }
         // The buffers by name in two copies of the step: the compiler then knows that
         // reads of one need not wait for the writes of the other.  Past the last block
         // scores are formed of whatever lies in LDS, and dropped.
-        const auto step = [&](int b, char *k, char *knext, char *v, char *vnext, f32x16 *s, f32x16 *next) {
+        const auto step = [&](int b, char *k, char *knext, char *v, char *vnext, f32x16 *s, f32x16 *next,
+                              typename Rows::Raw &xnow, typename Rows::Raw &xnext, typename Rows::Raw &ynow,
+                              typename Rows::Raw &ynext) {
             const int j0 = key(b);
             __syncthreads(); // block b's v and b + 1's k are there; b's k and b - 1's v are done with
-            const int id2 = t.at.checked(raw2);
-            // past the last block the last one's codes are widened again, and dropped
-            typename Rows::Raw x, y;
-            t.template ask<false>(key(min(b + 2, b1 - 1)), id2, x);
-            raw2 = raw_at(b + 3);
+            const int idl = t.at.checked(raw);
+            t.template ask<false>(last(b + kDeep + 2), idl, xnext);
+            raw = raw_at(b + kDeep + 3);
             const auto between = [&] {
-                if constexpr (F32OUT) // both pieces of the weights leave no registers for x among the products
-                    t.template put<false>(x, k);
-                t.template ask<true>(key(min(b + 1, b1 - 1)), id1, y);
+                if constexpr (F32OUT) // both pieces of the weights leave no registers for k's codes among the products
+                    t.template put<false>(xnow, k);
+                t.template ask<true>(last(b + kDeep + 1), idm, ynext);
             };
             const auto among = [&](int i) {
                 if constexpr (!F32OUT)
-                    t.template put<false>(x, k, i);
+                    t.template put<false>(xnow, k, i);
             };
             // one body for both kinds of block: in two, the sums would be copied between them
-            const bool part = !sees_all(a, t.p_lo, t.p_hi, j0, kBlock) || (has0 & kAll) != kAll;
+            const bool part = !sees_all(a, t.p_lo, t.p_hi, j0, kBlock) || (has[0] & kAll) != kAll;
             if (part)
-                t.clean(j0, has0, v);
+                t.clean(j0, has[0], v);
             if (t.live) {
-                t.block(j0, has0, knext, v, part, s, next, between, among);
+                t.block(j0, has[0], knext, v, part, s, next, between, among);
             } else {
                 between();
 #pragma unroll
                 for (int i = 0; i < 2 * Rows::kAsk; ++i)
                     among(i);
             }
-            t.template put<true>(y, vnext);
-            has0 = has1;
-            has1 = __ballot(id2 >= 0);
-            id1 = id2;
+            t.template put<true>(ynow, vnext);
+#pragma unroll
+            for (int i = 0; i < kDeep + 1; ++i)
+                has[i] = has[i + 1];
+            has[kDeep + 1] = __ballot(idl >= 0);
+            idm = idl;
         };
         for (int b = b0; b < b1; b += 2) {
-            step(b, ka, kb, va, vb, sa, sb);
+            step(b, ka, kb, va, vb, sa, sb, x[0], x[kDeep], y[0], y[kDeep]);
             if (b + 1 < b1)
-                step(b + 1, kb, ka, vb, va, sb, sa);
+                step(b + 1, kb, ka, vb, va, sb, sa, x[kDeep], x[0], y[kDeep], y[0]);
         }
         if (__syncthreads_or(t.special != 0))
             for (int b = b0; b < b1; ++b)
