@@ -9,6 +9,15 @@
 // the second wants it in.  For that, row m of the first product's two tiles is key
 // 8 (m / 4) + m % 4, and that + 4.  A lane's 16 bytes of k are 16 neighbouring values:
 // two steps of the product take them, and q is laid out alike.
+//
+// Memory-bound: 64 single tokens over up to 16384 keys of 8 heads of 128 (1.04 GB) take 209 us
+// in int8, 205 in e4m3 and 197 where a head's rows of a page lie together, 5.0 to 5.3 TB/s;
+// 294 us with two blocks ahead (which spilled), a product for every value of v and tiles of
+// one head.  More blocks ahead, or three or four workgroups a unit, gave nothing.
+// One token over 4099 keys takes 16.4 us, of which 8.5 are a call over one key (launch,
+// lengths, table, q) and the rest blocks, parts and their join; one over 131072 64 to 72.
+// Heads of 256 keep one block of k on its way and are bound by that: 269 us for 8192 keys,
+// 3.9 TB/s.
 #pragma once
 
 #include "paged8_attn_device.h"

@@ -21,6 +21,13 @@
 // The running maximum only moves when a row's new one is more than kSlack above it:
 // most blocks then skip the pass over the 32 x D sums.  A weight may then be up to
 // 2^kSlack, and the largest, which would be 1, is rounded like the others.
+//
+// 2048 tokens over 8192 keys, 32/8 heads of 128, take 266 to 277 us in e4m3 (868 to 902
+// TFLOP/s) and 300 in int8, 312 with binary16; the 16-bit cache's kernel 268.  Neither the
+// matrix cores (237 M of their cycles, 100 us of the time) nor the vector units (65 M
+// instructions, 120 us) are full: they wait for one another.  Without widening v it would be
+// 250: each tile widens all its codes itself.  Bank conflicts on the way into LDS cost 20 us
+// before rows were turned, k's widening ahead of the products 27.
 #pragma once
 
 #include "paged8_attn_device.h"
