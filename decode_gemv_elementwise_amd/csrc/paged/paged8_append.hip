@@ -238,15 +238,17 @@ __device__ __forceinline__ Target target_of(const Append8Args &a, int block, int
                   a.scales[v] + id * s[0] + div_by(a.block, in) * s[1] + head * s[2], c[1]};
 }
 
-// What a block holds beside the run, from scale byte `old` to the larger b, by `threads`
-// threads of which this is the i-th.  16 codes at a time.
-__device__ __forceinline__ void rescale(const Append8Args &a, const Run &r, const Target &to, int old, int b, int i, int threads)
+// What a block holds beside the run (taken(p): place p is one of its tokens'), from scale
+// byte `old` to the larger b, by `threads` threads of which this is the i-th.  16 codes at
+// a time.
+template <class F>
+__device__ __forceinline__ void rescale(const Append8Args &a, F taken, const Target &to, int old, int b, int i, int threads)
 {
     const int pieces = a.dim / 16;
     const float f = __builtin_bit_cast(float, (uint32_t)max(127 + old - b, 0) << 23); // a step so small leaves 0 either way
     for (int at = i; at < (int)a.block.d * pieces; at += threads) {
         const int p = at / pieces;
-        if (has_place(a, r, p))
+        if (taken(p))
             continue;
         u32x4 *const w = reinterpret_cast<u32x4 *>(to.codes + p * to.place + 16 * (at - p * pieces));
         u32x4 x = *w;
@@ -391,7 +393,7 @@ __device__ __forceinline__ void write_token(const Append8Args &a, const Run &r, 
         return;
     const int b = r.begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
     if (!r.begun && b > old && b < 255)
-        rescale(a, r, to, old, b, item, a.items.d);
+        rescale(a, [&](int p) { return has_place(a, r, p); }, to, old, b, item, a.items.d);
     if (item == 0)
         *to.scale = (uint8_t)b;
     put16(a, to.codes + (r.slot - r.block * (int)a.block.d) * to.place, p, x, inverse_of(b));
@@ -499,7 +501,7 @@ __global__ __launch_bounds__(kThreads) void paged8_append_kernel(Append8Args a)
                 }
                 const int b = begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
                 if (!begun && b > old && b < 255)
-                    rescale(a, part, to, old, b, me * kWave + lane, waves * kWave);
+                    rescale(a, [&](int p) { return has_place(a, part, p); }, to, old, b, me * kWave + lane, waves * kWave);
                 const float inv = inverse_of(b);
                 if (me == 0 && lane == 0)
                     *to.scale = (uint8_t)b;
@@ -541,7 +543,19 @@ template <class S> __global__ __launch_bounds__(kThreads) void paged8_append_gen
         return;
     }
     __shared__ uint32_t largest[kWaves];
+    __shared__ uint32_t taken[GEMV_PAGED_MAX_PAGE / 32]; // a bit for each place: a block may have too many to look for
     each_run(a, group_here(), [&](Run r, int share) {
+        if (!r.straight) {
+            for (int i = threadIdx.x; i < ((int)a.block.d + 31) / 32; i += kThreads)
+                taken[i] = 0;
+            __syncthreads();
+            for (int i = threadIdx.x; i < r.n; i += kThreads) {
+                const int p = a.slots[r.first + i] - r.block * (int)a.block.d;
+                atomicOr(&taken[p / 32], 1u << (p % 32));
+            }
+            __syncthreads();
+        }
+        const auto has = [&](int p) { return r.straight ? has_place(a, r, p) : (taken[p / 32] >> (p % 32) & 1) != 0; };
         const int last = min((share + 1) * a.kv_share, 2 * a.heads);
         for (int row = share * a.kv_share; row < last; ++row) {
             const int v = row >= a.heads, head = v ? row - a.heads : row;
@@ -560,7 +574,7 @@ template <class S> __global__ __launch_bounds__(kThreads) void paged8_append_gen
                 top = max(top, largest[w]);
             const int b = r.begun ? byte_of(a.e4m3, top) : max(byte_of(a.e4m3, top), old);
             if (!r.begun && b > old && b < 255)
-                rescale(a, r, to, old, b, threadIdx.x, kThreads);
+                rescale(a, has, to, old, b, threadIdx.x, kThreads);
             const float inv = inverse_of(b);
             if (threadIdx.x == 0)
                 *to.scale = (uint8_t)b;

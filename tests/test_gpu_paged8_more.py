@@ -358,3 +358,13 @@ def test_scales_of_a_page_far_apart(lens):
         far.copy_(getattr(c.c, name))
         setattr(c.c, name, far)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("code", ref.CODES)
+@pytest.mark.parametrize("rot", [0, 50])
+def test_append_large_block_in_any_order(code, rot):
+    """Thousands of tokens of one block in no order, among places that hold others and are rescaled."""
+    page = 4096
+    c = Cache(code, 4, page, page, 1, 64, seed=6)
+    slots = random.Random(3).sample(range(page + 1, 2 * page), 3000) + random.Random(4).sample(range(3 * page, 4 * page), 1000)
+    run_append(c, "f32", "bf16", slots, 1, rot)
