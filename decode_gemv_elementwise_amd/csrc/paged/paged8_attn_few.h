@@ -200,8 +200,8 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
             // a lane's scores are of the keys vrun, whose scales of k are asked for with v's
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[i] = s0[i] * (scale * scale_of(x.ks[RUNS ? 0 : i]));
-                p[4 + i] = s1[i] * (scale * scale_of(x.ks[RUNS ? 0 : 4 + i]));
+                p[i] = s0[i] * scale_of(x.ks[RUNS ? 0 : i]) * scale; // the scales' product may not fit where theirs do
+                p[4 + i] = s1[i] * scale_of(x.ks[RUNS ? 0 : 4 + i]) * scale;
             }
         }
         // every row of the tile sees every key of the block

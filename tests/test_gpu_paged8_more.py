@@ -368,3 +368,14 @@ def test_append_large_block_in_any_order(code, rot):
     c = Cache(code, 4, page, page, 1, 64, seed=6)
     slots = random.Random(3).sample(range(page + 1, 2 * page), 3000) + random.Random(4).sample(range(3 * page, 4 * page), 1000)
     run_append(c, "f32", "bf16", slots, 1, rot)
+
+
+@pytest.mark.parametrize("code", ref.CODES)
+@pytest.mark.parametrize("lens", [[(1, 70)], [(40, 90)]])
+def test_scales_whose_product_passes_32_bits(code, lens):
+    """Rows of q that are 0 weigh all keys alike, whatever the keys' scales and the softmax's."""
+    c = Case(lens, code, "bf16", 2, 1, 64, seed=3)
+    c.c.ks.fill_(240)
+    c.q.zero_()
+    c.scale = 2.0 ** 20
+    c.check(c.run())
