@@ -179,8 +179,12 @@ __device__ __forceinline__ int byte_of(bool e4m3, uint32_t bits)
     return max(1, e4m3 ? e - 8 + (m > 0x600000) : e - 6 + (m > 0x7e0000));
 }
 
-// 2^(127 - b); a block that is NaN needs no codes.
-__device__ __forceinline__ float inverse_of(int b) { return b == 255 ? 0.0f : __builtin_bit_cast(float, (uint32_t)(254 - b) << 23); }
+// 2^(127 - b); a block that is NaN needs no codes.  2^-127, for the largest scale, is below
+// the normal numbers: half the least of them.
+__device__ __forceinline__ float inverse_of(int b)
+{
+    return b == 255 ? 0.0f : __builtin_bit_cast(float, max((uint32_t)(254 - b) << 23, 0x00400000u));
+}
 
 // Tokens [first, first + n) of one block.
 struct Run {
