@@ -11,9 +11,10 @@
 namespace gemv {
 namespace {
 
-// The codes of k and v, and the scales of both.
+// The codes of k and v, and the scales of both; what a page holds of each.
 struct CacheSpans {
     Span k, v, ks, vs;
+    uint64_t k_page, v_page, ks_page, vs_page;
 };
 
 // Two tensors of the same extents share no element: their spans are apart, or they lie
@@ -32,6 +33,20 @@ bool twins_apart(Span x, Span y, const int64_t *xs, const int64_t *ys, const int
     const int64_t stride[4] = {xs[0], xs[1], xs[2], (int64_t)step};
     const int64_t extents[4] = {extent[0], extent[1], extent[2], 2};
     return strides_nest(stride, extents, 4, row);
+}
+
+// Codes and scales share no byte: their spans are apart, or a page carries its scales.
+// Then both have the page's stride, and counted from a page's first code, modulo that
+// stride, a page's scales lie behind its codes and before the next one's.
+bool pages_apart(Span codes, Span scales, const int64_t *cs, const int64_t *ss, uint64_t codes_page, uint64_t scales_page)
+{
+    if (!overlap(codes, scales))
+        return true;
+    const uint64_t step = (uint64_t)cs[0];
+    if (cs[0] != ss[0] || codes_page > step || scales_page > step || codes.hi == UINTPTR_MAX || scales.hi == UINTPTR_MAX)
+        return false; // the last two: no real buffer
+    const uint64_t off = scales.lo >= codes.lo ? (scales.lo - codes.lo) % step : step - 1 - (codes.lo - scales.lo - 1) % step;
+    return off >= codes_page && off <= step - scales_page;
 }
 
 int check_cache8(const gemv_kv_cache8 *c, CacheSpans *spans)
@@ -62,15 +77,23 @@ int check_cache8(const gemv_kv_cache8 *c, CacheSpans *spans)
     }
     if (!aligned(c->k, 16) || !aligned(c->v, 16))
         return GEMV_E_ALIGN;
-    const auto bytes = [](const int64_t *s, const int64_t *n, int64_t row) { // below 2^64: a sum of three products of 62 bits
+    // from dimension `from` on; below 2^64: a sum of three products of 62 bits
+    const auto bytes = [](const int64_t *s, const int64_t *n, int64_t row, int from) {
         uint64_t e = (uint64_t)row;
-        for (int d = 0; d < 3; ++d)
+        for (int d = from; d < 3; ++d)
             e += (uint64_t)(n[d] - 1) * (uint64_t)s[d];
         return e;
     };
-    *spans = CacheSpans{span_of(c->k, bytes(c->k_stride, extent, c->dim)), span_of(c->v, bytes(c->v_stride, extent, c->dim)),
-                        span_of(c->k_scale, bytes(c->ks_stride, scales, 1)),
-                        span_of(c->v_scale, bytes(c->vs_stride, scales, 1))};
+    const auto codes = [&](const int64_t *s, int from) { return bytes(s, extent, c->dim, from); };
+    const auto of_scales = [&](const int64_t *s, int from) { return bytes(s, scales, 1, from); };
+    *spans = CacheSpans{span_of(c->k, codes(c->k_stride, 0)),
+                        span_of(c->v, codes(c->v_stride, 0)),
+                        span_of(c->k_scale, of_scales(c->ks_stride, 0)),
+                        span_of(c->v_scale, of_scales(c->vs_stride, 0)),
+                        codes(c->k_stride, 1),
+                        codes(c->v_stride, 1),
+                        of_scales(c->ks_stride, 1),
+                        of_scales(c->vs_stride, 1)};
     return GEMV_OK;
 }
 
@@ -80,8 +103,11 @@ bool cache8_apart(const gemv_kv_cache8 *c, const CacheSpans &s)
     const int64_t extent[3] = {c->num_pages, c->page_size, c->heads};
     const int64_t scales[3] = {c->num_pages, c->page_size / c->block, c->heads};
     return twins_apart(s.k, s.v, c->k_stride, c->v_stride, extent, c->dim) &&
-           twins_apart(s.ks, s.vs, c->ks_stride, c->vs_stride, scales, 1) && !overlap(s.k, s.ks) && !overlap(s.k, s.vs) &&
-           !overlap(s.v, s.ks) && !overlap(s.v, s.vs);
+           twins_apart(s.ks, s.vs, c->ks_stride, c->vs_stride, scales, 1) &&
+           pages_apart(s.k, s.ks, c->k_stride, c->ks_stride, s.k_page, s.ks_page) &&
+           pages_apart(s.k, s.vs, c->k_stride, c->vs_stride, s.k_page, s.vs_page) &&
+           pages_apart(s.v, s.ks, c->v_stride, c->ks_stride, s.v_page, s.ks_page) &&
+           pages_apart(s.v, s.vs, c->v_stride, c->vs_stride, s.v_page, s.vs_page);
 }
 
 } // namespace

@@ -43,7 +43,10 @@ typedef enum { GEMV_KV_INT8 = 0, GEMV_KV_E4M3 = 1 } gemv_kv_code;
  * Those strides are positive, multiples of 16 and below 2^31 each, no two codes
  * share an address, and k and v are 16-byte aligned.  The scale of place s of page
  * b and head h is k_scale[b * ks_stride[0] + s / block * ks_stride[1] + h *
- * ks_stride[2]], strides positive and below 2^31, no two scales at one address. */
+ * ks_stride[2]], strides positive and below 2^31, no two scales at one address.  What
+ * is appended to has no byte twice among the four: they lie apart, or in one buffer, k
+ * and v (or the two scales) with the same strides a fixed step apart, codes and scales
+ * with the same page stride, so that a page may carry its scales. */
 typedef struct {
     void *k, *v;
     uint8_t *k_scale, *v_scale;
@@ -77,7 +80,8 @@ typedef struct {
  *  q, k, v, src_type, tokens, positions, axes, axis, inv_freq, rot, style, slots
  *              as for gemv_paged_append, tokens up to 2^30.
  *  q_out       [tokens][q_heads][dim], contiguous, 16-byte aligned.
- * q_out, the codes and the scales overlap no input and not one another.
+ * q_out overlaps no input and no part of the cache, from first to last byte, and the
+ * cache no input.
  * 16-byte aligned rows with strides of whole 16 bytes, and rot a multiple of 16
  * (GEMV_ROPE_HALVES) or 8 (GEMV_ROPE_PAIRS), take the wide path. */
 int gemv_paged8_append(const void *q, const void *k, const void *v, int src_type, int64_t tokens, int64_t q_heads,
