@@ -232,7 +232,9 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct FewRows {
             p[i] = __builtin_amdgcn_exp2f(BF ? p[i] - base : p[i] - base + kF16Lift);
             l += p[i];
             // bf16 has the range to take v's scale on the weight, a power of two: the codes
-            // need no product then.  Of a NaN scale only rows that see the key take it.
+            // need no product then.  Below 2^-126 it has fewer bits, down to none at 2^-134:
+            // there a code of 448 makes a part of 2^-117 at most, where float32 sums of parts
+            // end soon too.  Of a NaN scale only rows that see the key take it.
             if constexpr (BF)
                 p[i] = seen >> i & 1 ? p[i] * scale_of(x.vs[RUNS ? 0 : i]) : 0.0f;
         }

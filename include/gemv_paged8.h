@@ -118,10 +118,12 @@ int gemv_paged8_read_validate(const gemv_kv_cache8 *cache, const int32_t *slots,
  *  q_type      GEMV_W_F16 or GEMV_W_BF16: q's, and out's where that is not f32.
  *  cache       dim 64, 128 or 256.
  *  workspace   that of gemv_paged_attn (gemv_paged_attn_workspace); one may serve both.
- * A value that q's type does not hold (only binary16 has such) enters as it is or rounded
- * to that type.  Wide paths are for blocks of whole multiples of 8 tokens (calls
- * of few tokens a request) and for pages of whole multiples of 16 whose blocks divide or
- * are divided by 16 (calls of many); others find each key by itself. */
+ * A value that q's type does not hold (only binary16 has such: past 65504 an infinity, below
+ * 2^-14 fewer bits) enters as it is or rounded to that type, by what else is in the call: a
+ * caller cannot know which.  With bf16 a part w_j v_j that is below 2^-117, the row's largest
+ * weight taken as 1, may be taken as 0.  Wide paths are for blocks of whole multiples of 8
+ * tokens (calls of few tokens a request) and for pages of whole multiples of 16 whose
+ * blocks divide or are divided by 16 (calls of many); others find each key by itself. */
 int gemv_paged8_attn(const void *q, int q_type, int64_t q_token_stride, int64_t q_head_stride,
                      const gemv_kv_cache8 *cache, const int32_t *block_table, int64_t table_width,
                      int64_t table_stride, const int32_t *query_start, const int32_t *kv_len, int64_t requests,
