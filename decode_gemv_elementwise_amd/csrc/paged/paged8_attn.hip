@@ -7,15 +7,21 @@
 namespace gemv {
 namespace {
 
-// Which kind of row tile a call takes.  The host knows the counts of tokens and requests
-// and no lengths.  A pass of 16 rows over a request's keys is bound by memory the first
-// time and costs 0.4 to 0.8 of that again; one of 128 rows costs 1.4, for its products.  So
-// few rows where a request has two such passes of 16 or less on average, spread evenly or
-// all in one chunk.  Heads of 128 in e4m3, 4 a group, over 4096 keys: 8 requests of 4 tokens
-// 24 us by few rows, 27 by many, of 8 tokens 28 and 28, of 9 49 and 34; 128 of 4 tokens 215
-// and 285; 128 of one token and a chunk of 256 over 2048 keys 135 and 184, 32 and such a
-// chunk 66 and 68.  One request of 8 tokens over 32768 keys: 40 and 53; heads of 64 33 and
-// 51, of 256 92 and 87.
+// Which kind of row tile a call takes: one for the whole call, since the host knows the
+// counts of tokens and requests and no lengths.  Few rows where there are no more tokens
+// than requests, whatever the group, and where a request has two tiles of 16 rows or less on
+// average.  us by few rows and by many, 8 requests over 4096 keys, heads of 128 in e4m3:
+//     group 4, 8 key/value heads   20 rows 27 27   32 28 27   36 49 33   64 41 34   128 61 45
+//     group 7, 4                   21      20 27   35 30 31   49 28 32   70 37 39   133 52 35
+//     group 16, 2                  32      21 24   48 23 31   64 21 32   128 27 48
+//     group 64, 1                  128     20 44
+// so with few key/value heads it gives up early, and late with single tokens of such groups
+// (64 query heads over one, 16384 keys: 1 request 27 43, 8 35 54, 64 130 94).  The mean is
+// wrong where rows are spread unevenly: 512 single tokens over 100 keys and a chunk of 2000
+// go by few rows (256 162; over 512 keys 280 259), and so does a chunk of 2000 among 500
+// requests without tokens (213 74); 8 single tokens in a captured call of 512 go by many
+// (over 4096 keys 24 27, over 16384 66 82).  It is right for 64 over 16384 keys with a chunk
+// of 256 (584 693) or 2048 (1984 1107), and for 128 over 2048 with a chunk of 256 (136 177).
 bool takes_many(int64_t tokens, int64_t requests, int64_t group)
 {
     return tokens > requests && tokens * group > 2 * kAttnRows * requests;

@@ -27,7 +27,10 @@
 // matrix cores (237 M of their cycles, 100 us of the time) nor the vector units (65 M
 // instructions, 120 us) are full: they wait for one another.  Without widening v it would be
 // 250: each tile widens all its codes itself.  Bank conflicts on the way into LDS cost 20 us
-// before rows were turned, k's widening ahead of the products 27.
+// before rows were turned, k's widening ahead of the products 27.  A float32 result takes 355
+// (int8 380), for its second products; pages of 8 and 24, whose keys are found one by one,
+// 273 and 270.  2048 tokens over themselves 65, 8192 791: the plan counts every tile
+// of a request for its last one.
 #pragma once
 
 #include "paged8_attn_device.h"
@@ -347,7 +350,10 @@ template <int CODE, bool BF, int D, bool F32OUT, bool RUNS> struct ManyRows {
             by = 1.0f;
             off = BF ? 0.0f : -kF16Lift;
         }
-        u32x4 pf[2 * KT], pl[F32OUT ? 2 * KT : 1]; // the weights in pairs, and the second piece of them
+        // The weights in pairs, rounded to 16 bits as the product takes them, the largest too (of up to
+        // 2^kSlack it is no power of two), while l has them whole: 0.0023 of a bf16 result in all,
+        // 0.0017 with exact weights.  For a float32 result a second piece holds the rest.
+        u32x4 pf[2 * KT], pl[F32OUT ? 2 * KT : 1];
         // the other workgroup's wave on this SIMD widens its codes meanwhile, at the lower priority
         __builtin_amdgcn_s_setprio(1);
         scores(k, next, [&](int n) {

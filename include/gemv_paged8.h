@@ -76,14 +76,16 @@ typedef struct {
  * q is still written).  Tokens of one call whose slots lie in one block are
  * neighbours in the call (in any order), as gemv_paged_slots lays them out; where
  * others lie between them, that block's values are unspecified.  Two tokens of one slot
- * leave either's values, and those of their block may be rounded twice.
+ * leave, value by value, either's, and those of their block may be rounded twice.
  *  q, k, v, src_type, tokens, positions, axes, axis, inv_freq, rot, style, slots
  *              as for gemv_paged_append, tokens up to 2^30.
  *  q_out       [tokens][q_heads][dim], contiguous, 16-byte aligned.
  * q_out overlaps no input and no part of the cache, from first to last byte, and the
  * cache no input.
- * 16-byte aligned rows with strides of whole 16 bytes, and rot a multiple of 16
- * (GEMV_ROPE_HALVES) or 8 (GEMV_ROPE_PAIRS), take the wide path. */
+ * 16-byte aligned rows with strides of whole 16 bytes, rot a multiple of 16
+ * (GEMV_ROPE_HALVES) or 8 (GEMV_ROPE_PAIRS), and blocks of at most 16 floor(1024 / dim)
+ * tokens (256 at dim 64, 128 at 128, 64 at 256, 32 at 512) take the wide path; others are
+ * many times slower.  A token that makes its block's scale grow pays for the whole block. */
 int gemv_paged8_append(const void *q, const void *k, const void *v, int src_type, int64_t tokens, int64_t q_heads,
                        int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *positions, int64_t axes,
                        const int32_t *axis, const float *inv_freq, int64_t rot, int style, const int32_t *slots,
